@@ -250,6 +250,94 @@ dsa_status dsa_dense_mla_attn_causal(const uint16_t* q, const uint16_t* kv, int 
                                      uint16_t* out, float* lse, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The 4-bit latent cache.
+ *
+ * A row of DSA_Q4_ROW_BYTES = 416 bytes holds the 576 values that a bf16
+ * latent row holds in 1152:
+ *   [0, 256)    the 512 latent values, 4 bits each, as 64 little-endian
+ *               32-bit words of 8: value j of a word is nibble j/2 (j even)
+ *               or 4 + j/2 (j odd); code c stands for c - 8, in [-7, 7]
+ *   [256, 288)  one scale byte b for each 16 consecutive latent values:
+ *               s(b) = (1 + (b & 7) / 8) * 2^((b >> 3) - 18)
+ *   [288, 416)  the 64 rotary values, bf16
+ * A latent value is (c - 8) * s(b), exact in bf16. Quantising a group of 16:
+ * b is the smallest byte with 7 s(b) >= its largest magnitude (255 if none
+ * is: magnitudes above 7 s(255) = 107520 saturate), then x / s(b) to the
+ * nearest integer, ties to even. A NaN is stored as 0 and does not count
+ * towards the scale; an infinity saturates. Rotary values are rounded to
+ * bf16 and otherwise kept, NaN and infinities included. Any bytes are valid
+ * cache contents: no row gives a latent value that is not finite.
+ * Cache arrays must be 32-byte aligned. Serving layout, no counterpart in
+ * the pages (they keep the latent rows in 16 or 8 bits).
+ * ------------------------------------------------------------------------ */
+#define DSA_Q4_ROW_BYTES 416
+
+/* Element types of the calls that take more than one. */
+typedef enum { DSA_F32 = 0, DSA_BF16 = 1, DSA_F16 = 2 } dsa_dtype;
+
+/* Row i of x (n rows of 576 values of `dtype`, x_stride >= 576 elements
+ * apart: a slice of a fused projection's output will do) goes to pool row
+ * slots[i] (slots [n] int32, device) of pool [pool_rows, 416], quantised.
+ * A negative slot skips its row (padding); one >= pool_rows is skipped and
+ * reported as DSA_ERR_BAD_INDEX by dsa_get_device_error. Rows that no slot
+ * names are left as they were. Slots >= 0 must be distinct: a row named twice
+ * ends up with parts of either (no other row is touched). For a paged cache
+ * slots[i] = block_table[pos / page_size] * page_size + pos % page_size.
+ * n = 0 is a no-op. x and slots must not overlap the pool. */
+dsa_status dsa_latent_q4_append(const void* x, long long x_stride, int dtype, const int32_t* slots, int n,
+                                uint8_t* pool, int pool_rows, void* stream);
+
+/* out[i, 0..576) = the values of pool row rows[i] in bf16 (exact), for rows
+ * [n] int32 (device; repeats allowed). A negative entry gives a row of zeros;
+ * one >= pool_rows too, and is reported as DSA_ERR_BAD_INDEX. out [n, 576]
+ * bf16 is the layout of the attention calls' kv. n = 0 is a no-op. */
+dsa_status dsa_latent_q4_gather(const uint8_t* pool, int pool_rows, const int32_t* rows, int n, uint16_t* out,
+                                void* stream);
+
+/* Sparse MQA attention over the 4-bit cache. Each call is its bf16 namesake
+ * with the cache as kv_q4 [.., 416] bytes: dsa_sparse_mla_attn (kv_q4 [L,
+ * 416]), dsa_sparse_mla_attn_decode ([B, L_max, 416]),
+ * dsa_sparse_mla_attn_paged ([pool_rows, 416]) and
+ * dsa_sparse_mla_attn_varlen ([total_k, 416]); the same arguments, limits,
+ * errors and split workspace (dsa_sparse_mla_attn_split_workspace_size). The
+ * result is that of the bf16 call over the rows that dsa_latent_q4_gather
+ * gives, up to fp32 rounding order. */
+dsa_status dsa_sparse_mla_attn_q4(const uint16_t* q, const uint8_t* kv_q4, const int32_t* idx, int T, int L, int Hq,
+                                  int topk, float scale, uint16_t* out, float* lse, void* stream);
+dsa_status dsa_sparse_mla_attn_q4_decode(const uint16_t* q, const uint8_t* kv_q4, const int32_t* idx, int B,
+                                         int L_max, int Hq, int topk, float scale, uint16_t* out, float* lse,
+                                         void* workspace, size_t ws_bytes, void* stream);
+dsa_status dsa_sparse_mla_attn_q4_paged(const uint16_t* q, const uint8_t* kv_q4_pool, const int32_t* block_table,
+                                        const int32_t* idx, int T, int rows, int pool_rows, int bt_stride,
+                                        int max_blocks, int page_size, int Hq, int topk, float scale, uint16_t* out,
+                                        float* lse, void* workspace, size_t ws_bytes, void* stream);
+dsa_status dsa_sparse_mla_attn_q4_varlen(const uint16_t* q, const uint8_t* kv_q4, const int32_t* idx,
+                                         const int32_t* cu_q, const int32_t* cu_k, int nseq, int T, int total_k,
+                                         int Hq, int topk, float scale, uint16_t* out, float* lse, void* stream);
+
+/* Residual addition, root-mean-square norm and E4M3 output in one pass, for
+ * the rows in front of a projection: with h = x + residual (x alone when
+ * residual is NULL),
+ *   y = h * rsqrt(mean(h^2) + eps) * weight      (weight NULL: ones)
+ *   scale = max|y| / 448 (1 where all are zero), codes = E4M3(y / scale)
+ * as in dsa_quantize_e4m3_rows, with one scale a row (group = 0, scale [n]) or
+ * one for each 128 consecutive values (group = 128, scale [n, ceil(d / 128)]).
+ * x [n, d] rows x_stride >= d elements apart; residual, summed and normed [n,
+ * d] and weight [d] contiguous; all of `dtype`. summed (or NULL) receives h
+ * and normed (or NULL) y, each rounded once; codes [n, d] bytes. Sums, norm
+ * and y are fp32, and the norm is taken of the unrounded h: a row whose sum
+ * of squares is above fp32's range (|h| near 1e19) gives zeros. A NaN in a
+ * row makes its codes NaN. summed may be residual itself, or x itself when
+ * x_stride = d; any other overlap is DSA_ERR_INVALID_ARG. 1 <= d <= 16384;
+ * eps finite and > 0. Arrays need only be aligned to their elements (16
+ * bytes, and d a multiple of 8, is the fast case). n = 0 is a no-op. The
+ * pages place a norm before the projections without naming a form; this is
+ * the root-mean-square norm as its authors define it. */
+dsa_status dsa_rms_norm_quantize_e4m3_rows(const void* x, long long x_stride, const void* residual,
+                                           const void* weight, int dtype, int n, int d, float eps, int group,
+                                           uint8_t* codes, float* scale, void* summed, void* normed, void* stream);
+
+/* ------------------------------------------------------------------------
  * Decode: B sequences, one new query each, at position t = lens[b]-1 of its
  * own cache (the new token's key and latent row are already cached). Caches
  * are strided by L_max tokens per sequence. Same definitions as prefill with

@@ -11,6 +11,7 @@ Build the library first with `python -m long_context_03_b200.build` (or
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -24,6 +25,8 @@ LIB_PATH = os.path.join(_HERE, "libdsa_b200.so")
 D_QK = 576
 D_V = 512
 MAX_TOPK = 2048
+Q4_ROW_BYTES = 416  # a row of the 4-bit latent cache (layout in include/dsa.h)
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported shape", -3: "CUDA error",
           -4: "device wait timed out", -5: "workspace too small", -6: "index outside the cache"}
@@ -72,6 +75,14 @@ def lib() -> ctypes.CDLL:
             L.dsa_sparse_mla_attn_split_workspace_size.restype = SZ
             L.dsa_sparse_mla_attn_decode.argtypes = [P, P, P, I, I, I, I, F, P, P, P, SZ, P]
             L.dsa_index_topk_decode_noalloc.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P, P]
+            LL = ctypes.c_longlong
+            L.dsa_rms_norm_quantize_e4m3_rows.argtypes = [P, LL, P, P, I, I, I, F, I, P, P, P, P, P]
+            L.dsa_latent_q4_append.argtypes = [P, LL, I, P, I, P, I, P]
+            L.dsa_latent_q4_gather.argtypes = [P, I, P, I, P, P]
+            L.dsa_sparse_mla_attn_q4.argtypes = [P, P, P, I, I, I, I, F, P, P, P]
+            L.dsa_sparse_mla_attn_q4_decode.argtypes = [P, P, P, I, I, I, I, F, P, P, P, SZ, P]
+            L.dsa_sparse_mla_attn_q4_paged.argtypes = [P, P, P, P, I, I, I, I, I, I, I, I, F, P, P, P, SZ, P]
+            L.dsa_sparse_mla_attn_q4_varlen.argtypes = [P, P, P, P, P, I, I, I, I, I, F, P, P, P]
             L.dsa_get_device_error.argtypes = [P, ctypes.POINTER(ctypes.c_uint)]
             L.dsa_selftest_wait_timeout.argtypes = [ctypes.c_longlong, P]
             L.dsa_status_string.argtypes = [I]
@@ -86,6 +97,9 @@ def lib() -> ctypes.CDLL:
                          "dsa_index_scores", "dsa_sparse_mla_attn", "dsa_index_topk_decode",
                          "dsa_index_scores_decode", "dsa_sparse_mla_attn_decode", "dsa_get_device_error",
                          "dsa_index_topk_decode_noalloc", "dsa_index_topk_decode_paged",
+                         "dsa_rms_norm_quantize_e4m3_rows", "dsa_latent_q4_append", "dsa_latent_q4_gather",
+                         "dsa_sparse_mla_attn_q4", "dsa_sparse_mla_attn_q4_decode", "dsa_sparse_mla_attn_q4_paged",
+                         "dsa_sparse_mla_attn_q4_varlen",
                          "dsa_selftest_wait_timeout"):
                 getattr(L, name).restype = I
             _lib = L
@@ -419,6 +433,200 @@ def dense_mla_attn_causal(q, kv, scale: float, *, q0: int = 0, out=None, lse=Non
         _req(lse, "lse", torch.float32, (T, Hq))
     _check(lib().dsa_dense_mla_attn_causal(_ptr(q), _ptr(kv), T, L, q0, Hq, float(scale), _ptr(out), _ptr(lse),
                                            _stream(q.device)))
+    return out, lse
+
+
+# ------------------------------------------------- the 4-bit latent cache and the norm in front of it
+
+def _on(device):
+    """Makes `device` the current one for a call (the library launches on the current device)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _rows(x, name):
+    """Row stride of a 2-D CUDA tensor whose rows are contiguous (the rows may lie apart)."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dim() != 2:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected two dimensions")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {x.dtype}")
+    n, d = x.shape
+    if d > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    stride = x.stride(0) if n > 1 else d
+    if stride < d:
+        raise ValueError(f"{name} has rows that overlap")
+    return stride
+
+
+def rms_norm_quantize_e4m3_rows(x, weight=None, *, residual=None, eps: float = 1e-6, group: int = 0, codes=None,
+                                scale=None, summed=None, normed=None, want_normed: bool = False):
+    """h = x + residual, y = h * rsqrt(mean(h^2) + eps) * weight, then E4M3 codes of y with a scale of
+    absmax/448 for each row (group 0) or each 128 values (group 128), in one launch.
+
+    x [n, d] f32, bf16 or f16 (rows may lie apart), residual [n, d] and weight [d] of x's type or None
+    -> (codes uint8 [n, d], scale f32 [n] or [n, ceil(d / 128)], summed, normed): summed is h and normed y, in
+    x's type. summed is given back when there is a residual (or a tensor for it; residual itself serves in
+    place), normed when want_normed (or a tensor for it); else None."""
+    x_stride = _rows(x, "x")
+    n, d = x.shape
+    if residual is not None:
+        _req(residual, "residual", x.dtype, (n, d))
+    if weight is not None:
+        _req(weight, "weight", x.dtype, (d,))
+    if codes is None:
+        codes = torch.empty((n, d), dtype=torch.uint8, device=x.device)
+    codes8 = _u8(codes)
+    _req(codes8, "codes", torch.uint8, (n, d))
+    shape = (n, -(-d // group)) if group > 0 else (n,)
+    if scale is None:
+        scale = torch.empty(shape, dtype=torch.float32, device=x.device)
+    _req(scale, "scale", torch.float32, shape)
+    if summed is None and residual is not None:
+        summed = torch.empty((n, d), dtype=x.dtype, device=x.device)
+    if summed is not None:
+        _req(summed, "summed", x.dtype, (n, d))
+    if normed is None and want_normed:
+        normed = torch.empty((n, d), dtype=x.dtype, device=x.device)
+    if normed is not None:
+        _req(normed, "normed", x.dtype, (n, d))
+    _same_device(x.device, residual=residual, weight=weight, codes=codes, scale=scale, summed=summed, normed=normed)
+    with _on(x.device):
+        _check(lib().dsa_rms_norm_quantize_e4m3_rows(_ptr(x), x_stride, _ptr(residual), _ptr(weight),
+                                                     _DTYPES[x.dtype], n, d, float(eps), group, _ptr(codes8),
+                                                     _ptr(scale), _ptr(summed), _ptr(normed), _stream(x.device)))
+    return codes, scale, summed, normed
+
+
+def latent_q4_append(x, slots, pool):
+    """Quantise latent rows x [n, 576] (f32, bf16 or f16; rows may lie apart) to 4 bits into rows slots [n]
+    int32 of pool [.., 416] uint8 (any leading dimensions, counted as rows). A negative slot skips its row;
+    the others must be distinct. Returns pool."""
+    x_stride = _rows(x, "x")
+    n = x.shape[0]
+    if x.shape[1] != D_QK:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected {(n, D_QK)}")
+    _req(slots, "slots", torch.int32, (n,))
+    rows = _req_q4(pool, "pool")
+    _same_device(x.device, slots=slots, pool=pool)
+    with _on(x.device):
+        _check(lib().dsa_latent_q4_append(_ptr(x), x_stride, _DTYPES[x.dtype], _ptr(slots), n, _ptr(pool), rows,
+                                          _stream(x.device)))
+    return pool
+
+
+def latent_q4_gather(pool, rows, *, out=None):
+    """Rows [n] int32 of a 4-bit cache pool [.., 416] as bf16 [n, 576] (exact; zeros for a negative row)."""
+    pool_rows = _req_q4(pool, "pool")
+    n = rows.shape[0]
+    _req(rows, "rows", torch.int32, (n,))
+    if out is None:
+        out = torch.empty((n, D_QK), dtype=torch.bfloat16, device=pool.device)
+    _req(out, "out", torch.bfloat16, (n, D_QK))
+    _same_device(pool.device, rows=rows, out=out)
+    with _on(pool.device):
+        _check(lib().dsa_latent_q4_gather(_ptr(pool), pool_rows, _ptr(rows), n, _ptr(out), _stream(pool.device)))
+    return out
+
+
+def _req_q4(cache, name, lead=None) -> int:
+    """Checks a 4-bit cache [.., 416] (leading shape `lead` if given); its rows."""
+    _req(cache, name, torch.uint8)
+    if cache.dim() < 2 or cache.shape[-1] != Q4_ROW_BYTES or (lead is not None and tuple(cache.shape[:-1]) != lead):
+        raise ValueError(f"{name} has shape {tuple(cache.shape)}, expected rows of {Q4_ROW_BYTES} bytes")
+    rows = cache.numel() // Q4_ROW_BYTES
+    if rows >= 1 << 31:
+        raise ValueError(f"{name} has {rows} rows, at most 2^31 - 1 are addressed")
+    return rows
+
+
+def _q4_outputs(q, idx, out, lse, want_lse):
+    """Checks q and idx, makes out and lse where the caller gave none; (T, Hq, topk, out, lse)."""
+    T, Hq, _ = q.shape
+    topk = idx.shape[1]
+    _req(q, "q", torch.bfloat16, (T, Hq, D_QK))
+    _req(idx, "idx", torch.int32, (T, topk))
+    if out is None:
+        out = torch.empty((T, Hq, D_V), dtype=torch.bfloat16, device=q.device)
+    _req(out, "out", torch.bfloat16, (T, Hq, D_V))
+    if lse is None and want_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _req(lse, "lse", torch.float32, (T, Hq))
+    return T, Hq, topk, out, lse
+
+
+def sparse_mla_attn_q4(q, kv_q4, idx, scale: float, *, out=None, lse=None, want_lse: bool = False):
+    """sparse_mla_attn over a 4-bit cache kv_q4 [L, 416]: out [T, Hq, 512] bf16 (and lse [T, Hq] f32)."""
+    T, Hq, topk, out, lse = _q4_outputs(q, idx, out, lse, want_lse)
+    L = kv_q4.shape[0]
+    _req_q4(kv_q4, "kv_q4", (L,))
+    _same_device(q.device, kv_q4=kv_q4, idx=idx, out=out, lse=lse)
+    with _on(q.device):
+        _check(lib().dsa_sparse_mla_attn_q4(_ptr(q), _ptr(kv_q4), _ptr(idx), T, L, Hq, topk, float(scale),
+                                            _ptr(out), _ptr(lse), _stream(q.device)))
+    return out, lse
+
+
+def sparse_mla_attn_q4_decode(q, kv_q4, idx, scale: float, *, out=None, lse=None, want_lse: bool = False,
+                              split: bool = True, workspace=None):
+    """sparse_mla_attn_decode over a 4-bit cache kv_q4 [B, L_max, 416]."""
+    B, Hq, topk, out, lse = _q4_outputs(q, idx, out, lse, want_lse)
+    L_max = kv_q4.shape[1]
+    _req_q4(kv_q4, "kv_q4", (B, L_max))
+    ws, ws_bytes = _split_ws(split, workspace, B, topk, q.device)
+    _same_device(q.device, kv_q4=kv_q4, idx=idx, out=out, lse=lse, workspace=ws)
+    with _on(q.device):
+        _check(lib().dsa_sparse_mla_attn_q4_decode(_ptr(q), _ptr(kv_q4), _ptr(idx), B, L_max, Hq, topk,
+                                                   float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
+                                                   _stream(q.device)))
+    return out, lse
+
+
+def sparse_mla_attn_q4_paged(q, kv_q4_pool, block_table, idx, rows: int, scale: float, *, page_size: int = 64,
+                             out=None, lse=None, want_lse: bool = False, split: bool = False, workspace=None):
+    """sparse_mla_attn_paged over a pool [pool_rows, 416] of 4-bit rows; block_table [T, max_blocks] or
+    [1, max_blocks] int32."""
+    T, Hq, topk, out, lse = _q4_outputs(q, idx, out, lse, want_lse)
+    pool_rows = kv_q4_pool.shape[0]
+    nbt, max_blocks = block_table.shape
+    _req_q4(kv_q4_pool, "kv_q4_pool", (pool_rows,))
+    _req(block_table, "block_table", torch.int32, (nbt, max_blocks))
+    if nbt not in (1, T):
+        raise ValueError("block_table needs one row per token or a single shared row")
+    ws, ws_bytes = _split_ws(split, workspace, T, topk, q.device)
+    _same_device(q.device, kv_q4_pool=kv_q4_pool, block_table=block_table, idx=idx, out=out, lse=lse, workspace=ws)
+    with _on(q.device):
+        _check(lib().dsa_sparse_mla_attn_q4_paged(_ptr(q), _ptr(kv_q4_pool), _ptr(block_table), _ptr(idx), T, rows,
+                                                  pool_rows, 0 if nbt == 1 else max_blocks, max_blocks, page_size,
+                                                  Hq, topk, float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
+                                                  _stream(q.device)))
+    return out, lse
+
+
+def sparse_mla_attn_q4_varlen(q, kv_q4, idx, cu_q, cu_k, scale: float, *, out=None, lse=None,
+                              want_lse: bool = False):
+    """sparse_mla_attn_varlen over packed 4-bit rows kv_q4 [total_k, 416]."""
+    T, Hq, topk, out, lse = _q4_outputs(q, idx, out, lse, want_lse)
+    total_k = kv_q4.shape[0]
+    cu_q = torch.as_tensor(cu_q, dtype=torch.int32, device=q.device).contiguous()
+    cu_k = torch.as_tensor(cu_k, dtype=torch.int32, device=q.device).contiguous()
+    nseq = cu_q.numel() - 1
+    _req_q4(kv_q4, "kv_q4", (total_k,))
+    _req(cu_q, "cu_q", torch.int32, (nseq + 1,))
+    _req(cu_k, "cu_k", torch.int32, (nseq + 1,))
+    _same_device(q.device, kv_q4=kv_q4, idx=idx, out=out, lse=lse)
+    with _on(q.device):
+        _check(lib().dsa_sparse_mla_attn_q4_varlen(_ptr(q), _ptr(kv_q4), _ptr(idx), _ptr(cu_q), _ptr(cu_k), nseq, T,
+                                                   total_k, Hq, topk, float(scale), _ptr(out), _ptr(lse),
+                                                   _stream(q.device)))
     return out, lse
 
 

@@ -19,6 +19,9 @@
 #include "indexer_prefill.cuh"
 #include "sparse_mla.cuh"
 #include "quantize.cuh"
+#include "latent_q4.cuh"
+#include "rms_norm_quantize.cuh"
+#include "sparse_mla_q4.cuh"
 #include "topk_select.cuh"
 
 using namespace dsa;
@@ -492,6 +495,115 @@ dsa_status check_mla_args(const uint16_t* q, const uint16_t* kv, const int32_t* 
   return DSA_OK;
 }
 
+// ---- attention over the 4-bit latent cache ----
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+// Co-resident 2-CTA clusters of the 4-bit attention kernel (both instances
+// take the same resources), looked up once.
+int mla_q4_max_clusters() {
+  static std::atomic<int> cache{0};
+  int n = cache.load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * 512, 1, 1);
+    cfg.blockDim = dim3(MlaQ4Cfg::NTHREADS, 1, 1);
+    cfg.dynamicSmemBytes = MlaQ4Cfg::SMEM_BYTES;
+    if (set_smem(sparse_mla_q4_kernel<false>, MlaQ4Cfg::SMEM_BYTES) != DSA_OK ||
+        cudaOccupancyMaxActiveClusters(&n, sparse_mla_q4_kernel<false>, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = num_sms() / 2;
+    }
+    if (n > num_sms() / 2) n = num_sms() / 2;
+    if (n < 1) n = 1;
+    cache.store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+dsa_status launch_mla_q4(const uint16_t* q, const uint8_t* cache, const int32_t* idx, int T, int rows,
+                         long long token_rows, int Hq, int topk, float scale, uint16_t* out, float* lse,
+                         cudaStream_t st, MlaPaging pg = MlaPaging(), MlaPacked pk = MlaPacked(),
+                         float* part = nullptr) {
+  MlaQ4Params p = {};
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.cache = cache;
+  p.token_rows = token_rows;
+  p.idx = idx;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.rows = rows;
+  p.T = T;
+  p.Hq = Hq;
+  p.K = topk;
+  p.block_table = pg.block_table;
+  p.bt_stride = pg.bt_stride;
+  p.page_shift = pg.page_shift;
+  p.pool_rows = pg.pool_rows;
+  p.seq_cu_q = pk.cu_q;
+  p.seq_cu_k = pk.cu_k;
+  p.nseq = pk.nseq;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  CUtensorMap tmQ, tmO, tmP;
+  dsa_status s = make_map_q_bf16(&tmQ, q, T, Hq);
+  if (s != DSA_OK) return s;
+  s = make_map_out_bf16(&tmO, out, T, Hq);
+  if (s != DSA_OK) return s;
+  std::memset(&tmP, 0, sizeof(tmP));  // used only by split calls
+  auto kern = pg.block_table ? sparse_mla_q4_kernel<true> : sparse_mla_q4_kernel<false>;
+  s = set_smem(kern, MlaQ4Cfg::SMEM_BYTES);
+  if (s != DSA_OK) return s;
+  const int max_clusters = mla_q4_max_clusters();
+  const int nchunk = (topk + MlaCfg::NK - 1) / MlaCfg::NK;
+  const long long units = static_cast<long long>(T) * nchunk;
+  if (2 * T > max_clusters) part = nullptr;  // as launch_mla: larger batches fill the GPU with whole tokens
+  p.part = part;
+  const int nclusters = part ? static_cast<int>(units < max_clusters ? units : max_clusters)
+                             : (T < max_clusters ? T : max_clusters);
+  if (part) {
+    s = make_map_part_f32(&tmP, part, 2 * nclusters, Hq);
+    if (s != DSA_OK) return s;
+  }
+  const cudaError_t e = launch_dependent(kern, dim3(2 * nclusters), dim3(MlaQ4Cfg::NTHREADS), MlaQ4Cfg::SMEM_BYTES,
+                                         st, tmQ, tmO, tmP, p);
+  if (e != cudaSuccess) return cuda_fail(e, "sparse_mla_q4_kernel launch");
+  s = check_launch("sparse_mla_q4_kernel");
+  if (s != DSA_OK || !part) return s;
+  const int nsplit = mla_split_tokens(T, nchunk, nclusters, -1, nullptr);
+  if (nsplit == 0) return DSA_OK;
+  const dim3 cgrid(nsplit, (Hq + kCombineHeads - 1) / kCombineHeads);
+  const cudaError_t e2 = launch_dependent(mla_combine_kernel, cgrid, dim3(256), 0, st, part, T, nchunk, nclusters,
+                                          Hq, p.out, lse);
+  if (e2 != cudaSuccess) return cuda_fail(e2, "mla_combine_kernel launch");
+  return check_launch("mla_combine_kernel");
+}
+
+// The checks of the bf16 form, and the 4-bit rows' stricter alignment.
+dsa_status check_mla_q4_args(const uint16_t* q, const uint8_t* cache, const int32_t* idx, int T, int L, int Hq,
+                             int topk, float scale, const uint16_t* out) {
+  const dsa_status s = check_mla_args(q, reinterpret_cast<const uint16_t*>(cache), idx, T, L, Hq, topk, scale, out);
+  if (s != DSA_OK) return s;
+  if (!aligned32(cache)) return fail(DSA_ERR_INVALID_ARG, "4-bit cache not 32-byte aligned");
+  return DSA_OK;
+}
+
+// ---- norm ----
+template <typename T, bool kGroup>
+void launch_norm(const NormParams& p, cudaStream_t st) {
+  // One warp holds a row of up to 1024 values, one block a longer one.
+  auto go = [&](auto kern, int rows_per_block) {
+    kern<<<(p.n + rows_per_block - 1) / rows_per_block, kNormThreads, 0, st>>>(p);
+  };
+  if (p.d <= 256) go(rms_norm_quantize_kernel<T, 32, 1, kGroup>, 8);
+  else if (p.d <= 512) go(rms_norm_quantize_kernel<T, 32, 2, kGroup>, 8);
+  else if (p.d <= 1024) go(rms_norm_quantize_kernel<T, 32, 4, kGroup>, 8);
+  else if (p.d <= 2048) go(rms_norm_quantize_kernel<T, 256, 1, kGroup>, 1);
+  else if (p.d <= 4096) go(rms_norm_quantize_kernel<T, 256, 2, kGroup>, 1);
+  else if (p.d <= 8192) go(rms_norm_quantize_kernel<T, 256, 4, kGroup>, 1);
+  else go(rms_norm_quantize_kernel<T, 256, 8, kGroup>, 1);
+}
+
+int dtype_size(int dtype) { return dtype == DSA_F32 ? 4 : (dtype == DSA_BF16 || dtype == DSA_F16) ? 2 : 0; }
+
 }  // namespace
 
 extern "C" {
@@ -868,6 +980,169 @@ dsa_status dsa_sparse_mla_attn(const uint16_t* q, const uint16_t* kv, const int3
   if (s != DSA_OK) return s;
   if (T == 0) return DSA_OK;
   return launch_mla(q, kv, idx, T, L, 0, Hq, topk, scale, out, lse, static_cast<cudaStream_t>(stream));
+}
+
+dsa_status dsa_rms_norm_quantize_e4m3_rows(const void* x, long long x_stride, const void* residual,
+                                           const void* weight, int dtype, int n, int d, float eps, int group,
+                                           uint8_t* codes, float* scale, void* summed, void* normed, void* stream) {
+  const int es = dtype_size(dtype);
+  if (es == 0) return fail(DSA_ERR_UNSUPPORTED, "dtype=%d (DSA_F32, DSA_BF16 or DSA_F16)", dtype);
+  if (n < 0 || d <= 0) return fail(DSA_ERR_INVALID_ARG, "n=%d d=%d", n, d);
+  if (d > kNormMaxD) return fail(DSA_ERR_UNSUPPORTED, "d=%d above %d", d, kNormMaxD);
+  if (group != 0 && group != kNormGroup) return fail(DSA_ERR_UNSUPPORTED, "group=%d (0 or %d)", group, kNormGroup);
+  if (!std::isfinite(eps) || !(eps > 0.f)) return fail(DSA_ERR_INVALID_ARG, "eps must be finite and > 0");
+  if (x_stride < d) return fail(DSA_ERR_INVALID_ARG, "x_stride=%lld below d=%d", x_stride, d);
+  if (n == 0) return DSA_OK;
+  if (!x || !codes || !scale) return fail(DSA_ERR_INVALID_ARG, "null pointer");
+  const uintptr_t mask = static_cast<uintptr_t>(es - 1);
+  if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(residual) | reinterpret_cast<uintptr_t>(weight) |
+        reinterpret_cast<uintptr_t>(summed) | reinterpret_cast<uintptr_t>(normed)) & mask) ||
+      (reinterpret_cast<uintptr_t>(scale) & 3u))
+    return fail(DSA_ERR_INVALID_ARG, "an array is not aligned to its elements");
+  const size_t row = static_cast<size_t>(d) * es, nd = static_cast<size_t>(n) * d, dense = nd * es;
+  const size_t xb = (static_cast<size_t>(n) - 1) * static_cast<size_t>(x_stride) * es + row;
+  const size_t sb = static_cast<size_t>(n) * (group ? (d + group - 1) / group : 1) * 4;
+  struct Range { const void* p; size_t n; };
+  const Range in[3] = {{x, xb}, {residual, dense}, {weight, row}};
+  const Range outs[4] = {{codes, nd}, {scale, sb}, {summed, dense}, {normed, dense}};
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 3; ++i) {
+      // in place: the sum over the residual, or over x where its rows are contiguous
+      if (o == 2 && outs[o].p && (outs[o].p == residual ? i == 1 : (outs[o].p == x && x_stride == d && i == 0)))
+        continue;
+      if (overlaps(in[i].p, in[i].n, outs[o].p, outs[o].n))
+        return fail(DSA_ERR_INVALID_ARG, "an output overlaps an input (only summed may be residual or contiguous x)");
+    }
+    for (int k = 0; k < o; ++k)
+      if (overlaps(outs[k].p, outs[k].n, outs[o].p, outs[o].n))
+        return fail(DSA_ERR_INVALID_ARG, "two outputs overlap");
+  }
+  NormParams p = {};
+  p.x = x;
+  p.residual = residual;
+  p.weight = weight;
+  p.summed = summed;
+  p.normed = normed;
+  p.codes = codes;
+  p.scale = scale;
+  p.x_stride = x_stride;
+  p.n = n;
+  p.d = d;
+  p.eps = eps;
+  p.vec = d % 8 == 0 && (x_stride * es) % 16 == 0 && aligned16(x) && aligned16(residual) && aligned16(weight) &&
+          aligned16(summed) && aligned16(normed) && (reinterpret_cast<uintptr_t>(codes) & 7u) == 0;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == DSA_F32) group ? launch_norm<float, true>(p, st) : launch_norm<float, false>(p, st);
+  else if (dtype == DSA_BF16) group ? launch_norm<__nv_bfloat16, true>(p, st) : launch_norm<__nv_bfloat16, false>(p, st);
+  else group ? launch_norm<__half, true>(p, st) : launch_norm<__half, false>(p, st);
+  return check_launch("rms_norm_quantize_kernel");
+}
+
+dsa_status dsa_latent_q4_append(const void* x, long long x_stride, int dtype, const int32_t* slots, int n,
+                                uint8_t* pool, int pool_rows, void* stream) {
+  const int es = dtype_size(dtype);
+  if (es == 0) return fail(DSA_ERR_UNSUPPORTED, "dtype=%d (DSA_F32, DSA_BF16 or DSA_F16)", dtype);
+  if (n < 0 || pool_rows <= 0) return fail(DSA_ERR_INVALID_ARG, "n=%d pool_rows=%d", n, pool_rows);
+  if (x_stride < DSA_D_QK) return fail(DSA_ERR_INVALID_ARG, "x_stride=%lld below %d", x_stride, DSA_D_QK);
+  if (!pool || (n > 0 && (!x || !slots))) return fail(DSA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned32(pool)) return fail(DSA_ERR_INVALID_ARG, "4-bit cache not 32-byte aligned");
+  if (n == 0) return DSA_OK;
+  if ((reinterpret_cast<uintptr_t>(x) & static_cast<uintptr_t>(es - 1)) || (reinterpret_cast<uintptr_t>(slots) & 3u))
+    return fail(DSA_ERR_INVALID_ARG, "x or slots is not aligned to its elements");
+  const size_t pb = static_cast<size_t>(pool_rows) * kQ4RowBytes;
+  if (overlaps(x, ((static_cast<size_t>(n) - 1) * static_cast<size_t>(x_stride) + DSA_D_QK) * es, pool, pb) ||
+      overlaps(slots, static_cast<size_t>(n) * 4, pool, pb))
+    return fail(DSA_ERR_INVALID_ARG, "x or slots overlaps the pool");
+  const bool vec = aligned16(x) && (x_stride * es) % 16 == 0;
+  const int grid = n / (kQ4Threads / 32) + (n % (kQ4Threads / 32) ? 1 : 0);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == DSA_F32)
+    latent_q4_append_kernel<<<grid, kQ4Threads, 0, st>>>(static_cast<const float*>(x), x_stride, slots, n, pool_rows,
+                                                         vec, pool);
+  else if (dtype == DSA_BF16)
+    latent_q4_append_kernel<<<grid, kQ4Threads, 0, st>>>(static_cast<const __nv_bfloat16*>(x), x_stride, slots, n,
+                                                         pool_rows, vec, pool);
+  else
+    latent_q4_append_kernel<<<grid, kQ4Threads, 0, st>>>(static_cast<const __half*>(x), x_stride, slots, n, pool_rows,
+                                                         vec, pool);
+  return check_launch("latent_q4_append_kernel");
+}
+
+dsa_status dsa_latent_q4_gather(const uint8_t* pool, int pool_rows, const int32_t* rows, int n, uint16_t* out,
+                                void* stream) {
+  if (n < 0 || pool_rows <= 0) return fail(DSA_ERR_INVALID_ARG, "n=%d pool_rows=%d", n, pool_rows);
+  if (!pool || (n > 0 && (!rows || !out))) return fail(DSA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned32(pool) || !aligned16(out)) return fail(DSA_ERR_INVALID_ARG, "pool not 32-byte or out not 16-byte aligned");
+  if (n == 0) return DSA_OK;
+  if (reinterpret_cast<uintptr_t>(rows) & 3u) return fail(DSA_ERR_INVALID_ARG, "rows is not aligned to its elements");
+  const size_t ob = static_cast<size_t>(n) * DSA_D_QK * 2;
+  if (overlaps(out, ob, pool, static_cast<size_t>(pool_rows) * kQ4RowBytes) ||
+      overlaps(out, ob, rows, static_cast<size_t>(n) * 4))
+    return fail(DSA_ERR_INVALID_ARG, "out overlaps an input");
+  const int grid = n / (kQ4Threads / 32) + (n % (kQ4Threads / 32) ? 1 : 0);
+  latent_q4_gather_kernel<<<grid, kQ4Threads, 0, static_cast<cudaStream_t>(stream)>>>(
+      pool, pool_rows, rows, n, reinterpret_cast<__nv_bfloat16*>(out));
+  return check_launch("latent_q4_gather_kernel");
+}
+
+dsa_status dsa_sparse_mla_attn_q4(const uint16_t* q, const uint8_t* kv_q4, const int32_t* idx, int T, int L, int Hq,
+                                  int topk, float scale, uint16_t* out, float* lse, void* stream) {
+  const dsa_status s = check_mla_q4_args(q, kv_q4, idx, T, L, Hq, topk, scale, out);
+  if (s != DSA_OK || T == 0) return s;
+  return launch_mla_q4(q, kv_q4, idx, T, L, 0, Hq, topk, scale, out, lse, static_cast<cudaStream_t>(stream));
+}
+
+dsa_status dsa_sparse_mla_attn_q4_decode(const uint16_t* q, const uint8_t* kv_q4, const int32_t* idx, int B,
+                                         int L_max, int Hq, int topk, float scale, uint16_t* out, float* lse,
+                                         void* workspace, size_t ws_bytes, void* stream) {
+  dsa_status s = check_mla_q4_args(q, kv_q4, idx, B, L_max, Hq, topk, scale, out);
+  if (s != DSA_OK || B == 0) return s;
+  float* part = nullptr;
+  s = check_split_workspace(workspace, ws_bytes, B, topk, &part);
+  if (s != DSA_OK) return s;
+  return launch_mla_q4(q, kv_q4, idx, B, L_max, L_max, Hq, topk, scale, out, lse, static_cast<cudaStream_t>(stream),
+                       MlaPaging(), MlaPacked(), part);
+}
+
+dsa_status dsa_sparse_mla_attn_q4_paged(const uint16_t* q, const uint8_t* kv_q4_pool, const int32_t* block_table,
+                                        const int32_t* idx, int T, int rows, int pool_rows, int bt_stride,
+                                        int max_blocks, int page_size, int Hq, int topk, float scale, uint16_t* out,
+                                        float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  dsa_status s = check_mla_q4_args(q, kv_q4_pool, idx, T, rows, Hq, topk, scale, out);
+  if (s != DSA_OK) return s;
+  if (!block_table && T > 0) return fail(DSA_ERR_INVALID_ARG, "null pointer");
+  if (page_size < 16 || page_size > 4096 || (page_size & (page_size - 1)) != 0)
+    return fail(DSA_ERR_UNSUPPORTED, "page_size=%d (a power of two in [16, 4096])", page_size);
+  if (pool_rows <= 0 || bt_stride < 0 || max_blocks <= 0 || static_cast<long long>(max_blocks) * page_size < rows)
+    return fail(DSA_ERR_INVALID_ARG, "pool_rows=%d bt_stride=%d max_blocks=%d page_size=%d rows=%d", pool_rows,
+                bt_stride, max_blocks, page_size, rows);
+  if (T == 0) return DSA_OK;
+  float* part = nullptr;
+  s = check_split_workspace(workspace, ws_bytes, T, topk, &part);
+  if (s != DSA_OK) return s;
+  MlaPaging pg;
+  pg.block_table = block_table;
+  pg.bt_stride = bt_stride;
+  pg.page_shift = __builtin_ctz(static_cast<unsigned>(page_size));
+  pg.pool_rows = pool_rows;
+  return launch_mla_q4(q, kv_q4_pool, idx, T, rows, 0, Hq, topk, scale, out, lse, static_cast<cudaStream_t>(stream),
+                       pg, MlaPacked(), part);
+}
+
+dsa_status dsa_sparse_mla_attn_q4_varlen(const uint16_t* q, const uint8_t* kv_q4, const int32_t* idx,
+                                         const int32_t* cu_q, const int32_t* cu_k, int nseq, int T, int total_k,
+                                         int Hq, int topk, float scale, uint16_t* out, float* lse, void* stream) {
+  const dsa_status s = check_mla_q4_args(q, kv_q4, idx, T, total_k, Hq, topk, scale, out);
+  if (s != DSA_OK) return s;
+  if (nseq < 1) return fail(DSA_ERR_INVALID_ARG, "nseq=%d", nseq);
+  if (!cu_q || !cu_k) return fail(DSA_ERR_INVALID_ARG, "null pointer");
+  if (T == 0) return DSA_OK;
+  MlaPacked pk;
+  pk.cu_q = cu_q;
+  pk.cu_k = cu_k;
+  pk.nseq = nseq;
+  return launch_mla_q4(q, kv_q4, idx, T, total_k, 0, Hq, topk, scale, out, lse, static_cast<cudaStream_t>(stream),
+                       MlaPaging(), pk);
 }
 
 size_t dsa_index_topk_decode_workspace_size(int B, int L_max, int topk) {

@@ -1,0 +1,257 @@
+// Residual addition, root-mean-square norm and an E4M3 output with scales in
+// one pass over the rows:
+//     h = x + residual                        (x alone without a residual)
+//     y = h * rsqrt(mean(h^2) + eps) * weight
+//     scale = max|y| / 448 over the row or over each group of 128 values (1 where all are zero)
+//     code = E4M3(y / scale)                  nearest, ties to even
+// h, the sum of squares and y are fp32: the sum that goes out is rounded once
+// to x's type, while the norm is taken of the unrounded one. The quantiser's
+// steps are those of quantize_e4m3_rows on the fp32 y, so with fp32 rows and
+// y written out the two agree bit for bit.
+//
+// A row is read once: its values stay in registers between the two
+// reductions (sum of squares, largest magnitude) and the output. kTpr threads
+// hold a row, kNv groups of 8 values each.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "dsa_common.cuh"
+#include "latent_q4.cuh"
+
+namespace dsa {
+
+constexpr int kNormThreads = 256;
+constexpr int kNormMaxD = 256 * 8 * 8;  // the widest row the registers of a block hold
+constexpr int kNormGroup = 128;
+
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 b = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void from_f32(float* p, float v) { *p = v; }
+__device__ __forceinline__ void from_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void from_f32(__half* p, float v) { *p = __float2half_rn(v); }
+
+__device__ __forceinline__ uint8_t e4m3_code(float y, float sc) {
+  const float q = fminf(fmaxf(__fdiv_rn(y, sc), -448.f), 448.f);
+  return static_cast<uint8_t>(__nv_cvt_float_to_fp8(y == y ? q : y, __NV_SATFINITE, __NV_E4M3));
+}
+
+struct NormParams {
+  const void* x;         // [n, d], rows x_stride elements apart
+  const void* residual;  // [n, d] or null
+  const void* weight;    // [d] or null (ones)
+  void* summed;          // [n, d] or null: h in x's type (may be residual or x itself)
+  void* normed;          // [n, d] or null: y in x's type
+  uint8_t* codes;        // [n, d]
+  float* scale;          // [n] or [n, ceil(d / 128)]
+  long long x_stride;
+  int n, d;
+  float eps;
+  bool vec;              // every row is 16-byte aligned and d % 8 == 0
+};
+
+// kGroup: a scale for each 128 values instead of one for the row. Without
+// alignment (vec false) the threads take single elements, neighbours next to
+// each other, and only the map from registers to elements differs.
+template <typename T, int kTpr, int kNv, bool kGroup>
+__global__ void __launch_bounds__(kNormThreads) rms_norm_quantize_kernel(const NormParams p) {
+  constexpr int kRows = kNormThreads / kTpr;  // rows of a block
+  constexpr int kWarps = kTpr / 32;           // warps of a row
+  constexpr int kMaxGroups = kTpr * 8 * kNv / kNormGroup > 0 ? kTpr * 8 * kNv / kNormGroup : 1;
+  __shared__ float red[kRows][kWarps];
+  __shared__ float redm[kRows][kWarps];
+  __shared__ uint32_t gmax[kGroup ? kRows : 1][kGroup ? kMaxGroups : 1];
+  const int sub = static_cast<int>(threadIdx.x) / kTpr, t = static_cast<int>(threadIdx.x) % kTpr;
+  const int lane = t & 31, w = t >> 5;
+  const long long row = static_cast<long long>(blockIdx.x) * kRows + sub;
+  // a warp-wide row's block may end past the last row: those warps leave, and
+  // nothing below waits for them (a row of one warp meets no block barrier)
+  if (row >= p.n) return;
+  const int d = p.d;
+  const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
+  const T* res = p.residual ? static_cast<const T*>(p.residual) + row * d : nullptr;
+  const T* wt = static_cast<const T*>(p.weight);
+  auto at = [&](int i, int k) { return p.vec ? (t + kTpr * i) * 8 + k : (i * 8 + k) * kTpr + t; };
+  auto row_sync = [&]() {
+    if constexpr (kWarps > 1) __syncthreads();
+    else __syncwarp();
+  };
+
+  float h[kNv][8];
+#pragma unroll
+  for (int i = 0; i < kNv; ++i) {
+    if (p.vec) {
+      const int e = at(i, 0);
+      if (e < d) {
+        load8(x + e, h[i]);
+        if (res) {
+          float r[8];
+          load8(res + e, r);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) h[i][k] += r[k];
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[i][k] = 0.f;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int e = at(i, k);
+        h[i][k] = e < d ? to_f32(x[e]) + (res ? to_f32(res[e]) : 0.f) : 0.f;
+      }
+    }
+  }
+  if constexpr (kGroup) {
+    for (int g = t; g < kMaxGroups; g += kTpr) gmax[sub][g] = 0u;
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < kNv; ++i) {
+    float a = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a = __fmaf_rn(h[i][k], h[i][k], a);
+    ss += a;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+  if constexpr (kWarps > 1) {
+    if (lane == 0) red[sub][w] = ss;
+    row_sync();
+    ss = red[sub][0];
+#pragma unroll
+    for (int j = 1; j < kWarps; ++j) ss += red[sub][j];
+  } else {
+    row_sync();  // gmax is zeroed
+  }
+  const float rstd = __frsqrt_rn(__fdiv_rn(ss, static_cast<float>(d)) + p.eps);
+
+  if (p.summed) {
+    T* o = static_cast<T*>(p.summed) + row * d;
+#pragma unroll
+    for (int i = 0; i < kNv; ++i) {
+      if (p.vec) {
+        if (at(i, 0) < d) store8(o + at(i, 0), h[i]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (at(i, k) < d) from_f32(o + at(i, k), h[i][k]);
+      }
+    }
+  }
+  // y in place of h, and the largest magnitudes (fmaxf passes NaN over, as
+  // the plain quantiser does: such a value's code is NaN, its scale the others')
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < kNv; ++i) {
+    float wv[8];
+    if (p.vec) {
+      if (wt && at(i, 0) < d) {
+        load8(wt + at(i, 0), wv);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) wv[k] = 1.f;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) wv[k] = (wt && at(i, k) < d) ? to_f32(wt[at(i, k)]) : 1.f;
+    }
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      h[i][k] = h[i][k] * rstd * wv[k];
+      m = fmaxf(m, fabsf(h[i][k]));
+      if constexpr (kGroup) {
+        if (!p.vec) {
+          // 32 neighbouring elements lie in one group (magnitudes compare as their bits)
+          const uint32_t mk = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(0.f, fabsf(h[i][k]))));
+          if (lane == 0 && at(i, k) < d) atomicMax(&gmax[sub][at(i, k) / kNormGroup], mk);
+        }
+      }
+    }
+    if constexpr (kGroup) {
+      if (p.vec) {
+        // 16 neighbouring threads hold a group
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        if ((lane & 15) == 0 && at(i, 0) < d) gmax[sub][at(i, 0) / kNormGroup] = __float_as_uint(m);
+      }
+    } else {
+      amax = fmaxf(amax, m);
+    }
+  }
+  float sc = 1.f;
+  if constexpr (kGroup) {
+    row_sync();
+    const int groups = (d + kNormGroup - 1) / kNormGroup;
+    for (int g = t; g < groups; g += kTpr) {
+      const float m = __uint_as_float(gmax[sub][g]);
+      p.scale[row * groups + g] = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+    }
+  } else {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    if constexpr (kWarps > 1) {
+      if (lane == 0) redm[sub][w] = amax;
+      row_sync();
+      amax = redm[sub][0];
+#pragma unroll
+      for (int j = 1; j < kWarps; ++j) amax = fmaxf(amax, redm[sub][j]);
+    }
+    sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+    if (t == 0) p.scale[row] = sc;
+  }
+  uint8_t* cr = p.codes + row * d;
+  T* no = p.normed ? static_cast<T*>(p.normed) + row * d : nullptr;
+#pragma unroll
+  for (int i = 0; i < kNv; ++i) {
+    if (p.vec) {
+      const int e = at(i, 0);
+      if (e >= d) continue;
+      if constexpr (kGroup) {
+        const float m = __uint_as_float(gmax[sub][e / kNormGroup]);
+        sc = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+      }
+      if (no) store8(no + e, h[i]);
+      uint32_t c[2] = {0, 0};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) c[k >> 2] |= static_cast<uint32_t>(e4m3_code(h[i][k], sc)) << (8 * (k & 3));
+      *reinterpret_cast<uint2*>(cr + e) = make_uint2(c[0], c[1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int e = at(i, k);
+        if (e >= d) continue;
+        if constexpr (kGroup) {
+          const float m = __uint_as_float(gmax[sub][e / kNormGroup]);
+          sc = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+        }
+        if (no) from_f32(no + e, h[i][k]);
+        cr[e] = e4m3_code(h[i][k], sc);
+      }
+    }
+  }
+}
+
+}  // namespace dsa

@@ -1,0 +1,863 @@
+// Sparse MQA attention over selected rows of the 4-bit latent cache.
+//
+// The same mathematics as sparse_mla.cuh (z = scale Q C^T over 576 values,
+// u = softmax(z) C[:, 0:512], fp32 softmax and accumulation), with rows C that
+// are held in 416 bytes (latent_q4.cuh). Their values are exact in bf16, so
+// the tensor cores see exactly the rows that latent_q4_gather reads back, and
+// only the rounding of P to bf16 and the order of the fp32 sums separate the
+// result from the definition.
+//
+// Work split over a 2-CTA cluster as in sparse_mla.cuh: the score CTA keeps Q
+// in TMEM, computes S = Q C^T for 128 rows at a time and the softmax, and
+// sends P to the value CTA, which accumulates O += P V in its whole TMEM. New
+// here is how the operand tiles come about:
+//   * Eight producer warps in each CTA load codes and scales straight into
+//     registers, one whole chunk ahead of their use (a register set is
+//     reloaded with the next chunk's bytes as soon as it has been expanded),
+//     expand them to bf16 and store them into the swizzled tiles that the MMA
+//     reads. One thread takes the 64 values of one row in one slab: 32
+//     contiguous bytes of codes in one load, eight 16-byte stores that fall
+//     into eight different bank groups for eight neighbouring rows.
+//   * The latent slabs of a chunk go through two rings of three tiles, each
+//     filled by four of the warps (slabs 0-3 and 4-7); the rotary slab (bf16 as
+//     it stands) has two tiles of its own. Q's tiles pass through both rings.
+//     A parity tells a phase only from its neighbours, so nobody may be two
+//     uses of a slot ahead or behind: the warp that loads Q also takes part in
+//     filling every other tile (one arrival, after it has seen the slot free),
+//     and the producers pass over Q's uses only once a barrier of its own says
+//     that Q is in TMEM.
+//   * Page lookups and range checks are made once a token, when the index row
+//     is staged: the row numbers in shared memory are final (-1 for absent).
+//     Absent rows are expanded from code 8, which is zero at any scale.
+//   * Sixteen warps do not fit the softmax's registers at an even share, so
+//     the warp groups trade registers at the start.
+#pragma once
+
+#include "dsa_common.cuh"
+#include "latent_q4.cuh"
+#include "sparse_mla.cuh"
+
+namespace dsa {
+
+struct MlaQ4Cfg {
+  static constexpr int NK = MlaCfg::NK;
+  static constexpr int SLAB_TILE = MlaCfg::SLAB_TILE;  // 128 rows x 128 bytes
+  static constexpr int NLAT = 8;                       // latent slabs of 64 values
+  static constexpr int NLST = 3;                       // tiles of each of the two latent rings (score CTA)
+  static constexpr int NRST = 2;                       // rotary tiles (score CTA)
+  static constexpr int VROWS = MlaCfg::VROWS;
+  static constexpr int VSLAB = MlaCfg::VSLAB;
+  static constexpr int V_TILE = MlaCfg::V_TILE;
+  static constexpr int NVST = 4;                       // value sub-tile ring (value CTA)
+  static constexpr int NPB = MlaCfg::NPB;
+  static constexpr int NPROD = 8;                      // producer warps
+  static constexpr int W_SM0 = 8;                      // four softmax / epilogue warps
+  static constexpr int W_MMA = 12;
+  static constexpr int W_Q = 13;                       // loads Q's tiles (score CTA)
+  static constexpr int NTHREADS = 16 * 32;
+  // registers a thread after the trade: 2 * 112 + 208 + 72 <= 4 * 128
+  static constexpr int REG_PROD = 112, REG_SM = 208, REG_MMA = 72;
+  static constexpr int OFF_RING = 0;
+  static constexpr int OFF_ROPE = 2 * NLST * SLAB_TILE;  // score CTA
+  static constexpr int RING_BYTES = (2 * NLST + NRST) * SLAB_TILE;
+  static_assert(RING_BYTES >= NVST * V_TILE, "the value ring shares the space");
+  static constexpr int MSG_STRIDE = MlaCfg::MSG_STRIDE;
+  static constexpr int OFF_MSG = OFF_RING + RING_BYTES;
+  static constexpr int OFF_IDX = OFF_MSG + NPB * MSG_STRIDE;
+  static constexpr int OFF_VMASK = OFF_IDX + MlaCfg::KMAX * 4;  // u32 [2][KMAX / 32]
+  static constexpr int OFF_EPI = (OFF_VMASK + 2 * (MlaCfg::KMAX / 32) * 4 + 1023) / 1024 * 1024;
+  static constexpr int EPI_TILE = MlaCfg::EPI_TILE;
+  static constexpr int OFF_BAR = OFF_EPI + 4 * 2 * EPI_TILE;
+  // barriers (the same offsets in both CTAs)
+  static constexpr int NRING = 2 * NLST;                  // score: ring g's slots from g * NLST; value: [NVST] sub-tiles
+  static_assert(NRING >= NVST, "one set of barriers serves both CTAs");
+  static constexpr int B_RING_FULL = 0;
+  static constexpr int B_RING_EMPTY = B_RING_FULL + NRING;
+  static constexpr int B_ROPE_FULL = B_RING_EMPTY + NRING;  // [NRST]
+  static constexpr int B_ROPE_EMPTY = B_ROPE_FULL + NRST;
+  static constexpr int B_S_FULL = B_ROPE_EMPTY + NRST;
+  static constexpr int B_S_EMPTY = B_S_FULL + 1;
+  static constexpr int B_Q_FREE = B_S_EMPTY + 1;
+  static constexpr int B_Q_IN = B_Q_FREE + 1;
+  static constexpr int B_P_FREE = B_Q_IN + 1;              // [NPB]
+  static constexpr int B_P_FULL = B_P_FREE + NPB;          // [NPB]
+  static constexpr int B_O_READY = B_P_FULL + NPB;         // [NPB]
+  static constexpr int B_PV_DONE = B_O_READY + NPB;
+  static constexpr int B_STAGE = B_PV_DONE + 1;
+  static constexpr int B_QUIESCE = B_STAGE + 1;
+  static constexpr int B_MASK_FULL = B_QUIESCE + 1;        // [2]
+  static constexpr int B_MASK_FREE = B_MASK_FULL + 2;      // [2]
+  static constexpr int B_PSTAGE = B_MASK_FREE + 2;
+  static constexpr int NBAR = B_PSTAGE + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 32;
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(2 * REG_PROD + REG_SM + REG_MMA <= 4 * (65536 / NTHREADS), "register trade");
+};
+
+// The base parameters' kv and kv_token_stride are unused; rows, paging and
+// packed-batch fields mean the same, in rows of kQ4RowBytes.
+struct MlaQ4Params : MlaParams {
+  const uint8_t* cache;   // pool or contiguous rows
+  long long token_rows;   // rows between consecutive tokens' caches (0: one shared cache)
+};
+
+template <int kRegs>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// Position in a ring of N slots: slot and the parity of its current pass.
+template <int N>
+struct RingPos {
+  int slot = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void step(int n) {
+    slot += n;
+    while (slot >= N) {
+      slot -= N;
+      ph ^= 1u;
+    }
+  }
+};
+
+__device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+
+// 64 values of a row (8 words of codes, 4 scale bytes) into its 128 bytes of a
+// swizzled tile: 16-byte piece c goes to c ^ (row & 7).
+__device__ __forceinline__ void expand_row(uint32_t row_addr, uint32_t swz, const uint32_t (&codes)[8],
+                                           uint32_t scales) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t s2 = q4_scale_pair((scales >> (8 * g)) & 0xffu);
+    const uint32_t off2 = q4_offset_pair(s2);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v[4];
+      q4_values(codes[2 * g + h], s2, off2, v);
+      sts128(row_addr + (static_cast<uint32_t>((2 * g + h) << 4) ^ swz), v);
+    }
+  }
+}
+
+// A row's 32 bytes at `off`, or codes of zero for an absent row.
+__device__ __forceinline__ void load_codes(uint32_t (&r)[8], const uint8_t* row, int off) {
+  if (row) {
+    ldg256(row + off, r);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[k] = 0x88888888u;
+  }
+}
+
+// First row and row count of token tk's cache, in rows of the cache array.
+__device__ __forceinline__ void token_rows_q4(const MlaQ4Params& p, int tk, long long& first, int& rows) {
+  if (p.seq_cu_q) {
+    int lo = 0, hi = p.nseq - 1;  // the last sequence whose first query is at or before tk
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldg(p.seq_cu_q + mid) <= tk) lo = mid;
+      else hi = mid - 1;
+    }
+    const int k0 = min(max(__ldg(p.seq_cu_k + lo), 0), p.rows);
+    const int k1 = min(max(__ldg(p.seq_cu_k + lo + 1), k0), p.rows);
+    first = k0;
+    rows = k1 - k0;
+  } else {
+    first = tk * p.token_rows;
+    rows = p.rows;
+  }
+}
+
+// The producer warps put a token's selection into shared memory as row
+// numbers from the token's first row (of the pool when paged), -1 where there
+// is none: past topk, negative, outside the cache or behind a page outside
+// the pool (both reported). Its threads meet twice on the mbarrier `stage`
+// (the previous row is no longer read; the new one is written), with bounded
+// waits. Writes the validity bits of each 32 entries when vmask is given.
+template <bool kPaged>
+__device__ __forceinline__ bool stage_rows_q4(int32_t* idx_s, uint32_t* vmask, const MlaQ4Params& p, int tk, int nent,
+                                              int rows, int ptid, uint64_t* stage, uint32_t& phase, AbortFlag ab) {
+  mbar_arrive(stage);
+  if (!mbar_wait(stage, phase, ab, 126)) return false;
+  phase ^= 1u;
+  const int32_t* src = p.idx + static_cast<size_t>(tk) * p.K;
+  for (int e = ptid; e < nent; e += MlaQ4Cfg::NPROD * 32) {  // nent is a multiple of 32: whole warps
+    int row = e < p.K ? __ldg(src + e) : -1;
+    bool bad = row >= rows;
+    if constexpr (kPaged) {
+      if (row >= 0 && !bad) {
+        const int page = __ldg(p.block_table + static_cast<long long>(tk) * p.bt_stride + (row >> p.page_shift));
+        const long long phys =
+            (static_cast<long long>(page) << p.page_shift) + (row & ((1 << p.page_shift) - 1));
+        bad = page < 0 || phys >= p.pool_rows;
+        row = static_cast<int>(phys);
+      }
+    }
+    if (bad) {
+      set_device_error(kErrBadIndex, 4);
+      row = -1;
+    }
+    row = max(row, -1);
+    idx_s[e] = row;
+    if (vmask) {
+      const uint32_t m = __ballot_sync(0xffffffffu, row >= 0);
+      if ((e & 31) == 0) vmask[e >> 5] = m;
+    }
+  }
+  mbar_arrive(stage);
+  if (!mbar_wait(stage, phase, ab, 127)) return false;
+  phase ^= 1u;
+  return true;
+}
+
+template <bool kPaged>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 1)
+    sparse_mla_q4_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
+                         const __grid_constant__ CUtensorMap tmP, const MlaQ4Params p) {
+  using C = MlaQ4Cfg;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  int* abort_s = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
+  int* rescale_s = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);
+  int32_t* idx_s = reinterpret_cast<int32_t*>(smem + C::OFF_IDX);
+  uint32_t* vmask_s = reinterpret_cast<uint32_t*>(smem + C::OFF_VMASK);
+  const AbortFlag ab{abort_s};
+  const uint32_t rank = cluster_ctarank();
+  const uint32_t warp = warp_id();
+  const uint32_t lane = lane_id();
+  const int cluster_id = blockIdx.x >> 1;
+  const int nclusters = gridDim.x >> 1;
+  const int nchunk = (p.K + C::NK - 1) / C::NK;
+  const MlaSegIter segs0(p, cluster_id, nclusters, nchunk);
+  const int total_msgs = segs0.messages();
+
+  if (threadIdx.x == 0) {
+    *abort_s = 0;
+    rescale_s[0] = 0;
+    rescale_s[1] = 0;
+    for (int i = 0; i < C::NRING; ++i) {
+      // arrivals: four producer warps and Q's a latent tile, eight a value sub-tile
+      mbar_init(bars + C::B_RING_FULL + i, rank == 0 ? C::NPROD / 2 + 1 : C::NPROD);
+      mbar_init(bars + C::B_RING_EMPTY + i, 1);
+    }
+    for (int i = 0; i < C::NRST; ++i) {
+      mbar_init(bars + C::B_ROPE_FULL + i, C::NPROD);
+      mbar_init(bars + C::B_ROPE_EMPTY + i, 1);
+    }
+    mbar_init(bars + C::B_S_FULL, 1);
+    mbar_init(bars + C::B_S_EMPTY, 4);
+    mbar_init(bars + C::B_Q_FREE, 1);
+    mbar_init(bars + C::B_Q_IN, 1);
+    for (int i = 0; i < C::NPB; ++i) {
+      mbar_init(bars + C::B_P_FREE + i, 1);
+      mbar_init(bars + C::B_P_FULL + i, 1);
+      mbar_init(bars + C::B_O_READY + i, 4);
+    }
+    mbar_init(bars + C::B_PV_DONE, 1);
+    mbar_init(bars + C::B_STAGE, 4);
+    mbar_init(bars + C::B_QUIESCE, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars + C::B_MASK_FULL + i, C::NPROD);
+      mbar_init(bars + C::B_MASK_FREE + i, 4);
+    }
+    mbar_init(bars + C::B_PSTAGE, C::NPROD * 32);
+    fence_mbar_init();
+  }
+  if (warp == C::W_MMA) tmem_alloc(tmem_base_s, 512);
+  __syncthreads();
+  griddep_launch_dependents();
+  // Value CTA: arm the first use of each P receive buffer before the peer can send.
+  if (rank == 1 && threadIdx.x == 0) {
+    for (int i = 0; i < C::NPB && i < total_msgs; ++i) {
+      const bool last = segs0.last_of_piece(i);
+      mbar_arrive_expect_tx(bars + C::B_P_FULL + i, last ? MlaCfg::MSG_BYTES_LAST : MlaCfg::MSG_BYTES_MID);
+    }
+  }
+  cluster_sync_all();
+  griddep_wait();  // nothing of global memory is touched before
+  tc_fence_after();
+  const uint32_t tmem = *tmem_base_s;
+  const uint32_t ring = smem_u32(smem + C::OFF_RING);
+  const uint32_t rope_ring = smem_u32(smem + C::OFF_ROPE);
+  const uint32_t msg = smem_u32(smem + C::OFF_MSG);
+
+  if (warp < C::NPROD) {
+    regs_down<C::REG_PROD>();
+    const int ptid = threadIdx.x;
+    uint32_t stage_ph = 0;
+    MlaSegIter segs = segs0;
+    MlaSeg sg;
+    if (rank == 0) {
+      // ---- score CTA: latent tiles (row r of the chunk, slabs 4 grp ..) and rotary tiles ----
+      const int grp = ptid >> 7;
+      const int r = ptid & 127;
+      const uint32_t swz = static_cast<uint32_t>(r & 7) << 4;
+      const int rc = ptid & 7, rr = ptid >> 3;  // rotary: piece rc of rows rr + 32 k
+      RingPos<C::NLST> lp;  // of this group's ring
+      uint64_t* lfull = bars + C::B_RING_FULL + grp * C::NLST;
+      uint64_t* lempty = bars + C::B_RING_EMPTY + grp * C::NLST;
+      const uint32_t lring = ring + grp * C::NLST * C::SLAB_TILE + r * 128;
+      RingPos<C::NRST> rp;
+      int n = 0;
+      bool ok = true;
+      for (; ok && segs.next(sg); ++n) {
+        long long first;
+        int trows;
+        token_rows_q4(p, sg.tk, first, trows);
+        const uint8_t* base = p.cache + first * kQ4RowBytes;
+        const int mb = n & 1;
+        if (!mbar_wait(bars + C::B_MASK_FREE + mb, ((n >> 1) & 1) ^ 1, ab, 130)) break;
+        if (!stage_rows_q4<kPaged>(idx_s, vmask_s + mb * (MlaCfg::KMAX / 32), p, sg.tk, nchunk * C::NK, trows, ptid,
+                                   bars + C::B_PSTAGE, stage_ph, ab))
+          break;
+        if (lane == 0) mbar_arrive(bars + C::B_MASK_FULL + mb);
+        auto row_of = [&](int j) -> const uint8_t* {
+          const int row = idx_s[j * C::NK + r];
+          return row >= 0 ? base + static_cast<long long>(row) * kQ4RowBytes : nullptr;
+        };
+        uint32_t codes[4][8];
+        uint4 sc, rope[4];
+        auto load_scales = [&](const uint8_t* row) {
+          return row ? ldg128(row + kQ4Scales + 16 * grp) : make_uint4(0, 0, 0, 0);
+        };
+        auto load_rope = [&](int j) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = idx_s[j * C::NK + rr + 32 * k];
+            rope[k] = row >= 0 ? ldg128(base + static_cast<long long>(row) * kQ4RowBytes + kQ4Rope + 16 * rc)
+                               : make_uint4(0, 0, 0, 0);
+          }
+        };
+        {
+          const uint8_t* row = row_of(sg.c0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) load_codes(codes[i], row, (4 * grp + i) * 32);
+          sc = load_scales(row);
+          load_rope(sg.c0);
+        }
+        // Q's tiles go first (five through ring 0, four through ring 1)
+        if (!mbar_wait(bars + C::B_Q_IN, n & 1, ab, 125)) break;
+        lp.step((MlaCfg::NSLAB_QK + 1 - grp) / 2);
+        for (int j = sg.c0; j < sg.c1; ++j) {
+          const bool more = j + 1 < sg.c1;
+          // rotary tile
+          if (!mbar_wait(bars + C::B_ROPE_EMPTY + rp.slot, rp.ph ^ 1u, ab, 132)) { ok = false; break; }
+          const uint32_t rt = rope_ring + rp.slot * C::SLAB_TILE;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = rr + 32 * k;
+            const uint32_t v[4] = {rope[k].x, rope[k].y, rope[k].z, rope[k].w};
+            sts128(rt + row * 128 + ((rc ^ (row & 7)) << 4), v);
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + C::B_ROPE_FULL + rp.slot);
+          rp.step(1);
+          const uint8_t* nrow = nullptr;
+          uint4 sc_next = make_uint4(0, 0, 0, 0);
+          if (more) {
+            load_rope(j + 1);
+            nrow = row_of(j + 1);
+            sc_next = load_scales(nrow);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (!mbar_wait(lempty + lp.slot, lp.ph ^ 1u, ab, 131)) { ok = false; break; }
+            const uint32_t s4 = i == 0 ? sc.x : i == 1 ? sc.y : i == 2 ? sc.z : sc.w;
+            expand_row(lring + lp.slot * C::SLAB_TILE, swz, codes[i], s4);
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(lfull + lp.slot);
+            if (more) load_codes(codes[i], nrow, (4 * grp + i) * 32);
+            lp.step(1);
+          }
+          if (!ok) break;
+          sc = sc_next;
+        }
+      }
+    } else {
+      // ---- value CTA: 32-row sub-tiles; warp = slab, lane = row ----
+      const uint32_t swz = (lane & 7u) << 4;
+      const uint32_t row_off = warp * C::VSLAB + lane * 128;
+      RingPos<C::NVST> vp;
+      bool ok = true;
+      while (ok && segs.next(sg)) {
+        long long first;
+        int trows;
+        token_rows_q4(p, sg.tk, first, trows);
+        const uint8_t* base = p.cache + first * kQ4RowBytes;
+        if (!stage_rows_q4<kPaged>(idx_s, nullptr, p, sg.tk, nchunk * C::NK, trows, ptid, bars + C::B_PSTAGE,
+                                   stage_ph, ab))
+          break;
+        uint32_t codes[4][8], sc[4];
+        auto load_sub = [&](int j, int u) {
+          const int row = idx_s[j * C::NK + u * C::VROWS + static_cast<int>(lane)];
+          const uint8_t* rp = row >= 0 ? base + static_cast<long long>(row) * kQ4RowBytes : nullptr;
+          load_codes(codes[u], rp, static_cast<int>(warp) * 32);
+          sc[u] = rp ? ldg32(rp + kQ4Scales + 4 * warp) : 0u;
+        };
+#pragma unroll
+        for (int u = 0; u < 4; ++u) load_sub(sg.c0, u);
+        for (int j = sg.c0; ok && j < sg.c1; ++j) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if (!mbar_wait(bars + C::B_RING_EMPTY + vp.slot, vp.ph ^ 1u, ab, 141)) { ok = false; break; }
+            expand_row(ring + vp.slot * C::V_TILE + row_off, swz, codes[u], sc[u]);
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + C::B_RING_FULL + vp.slot);
+            if (j + 1 < sg.c1) load_sub(j + 1, u);
+            vp.step(1);
+          }
+        }
+      }
+    }
+  } else if (warp >= C::W_MMA) {
+    regs_down<C::REG_MMA>();
+    if (warp == C::W_Q && rank == 0) {
+      // ---- Q[tk] as nine TMA tiles (heads >= Hq arrive as zeros), tile i through ring i & 1 ----
+      RingPos<C::NLST> lp[2];
+      MlaSegIter segs = segs0;
+      MlaSeg sg;
+      bool ok = true;
+      RingPos<C::NLST> q_at[2];  // where the last token's Q tiles start and how many were issued
+      int q_issued = 0;
+      while (ok && segs.next(sg)) {
+        for (int i = 0; ok && i < MlaCfg::NSLAB_QK; ++i) {
+          RingPos<C::NLST>& at = (i & 1) ? lp[1] : lp[0];
+          const int slot = (i & 1) * C::NLST + at.slot;
+          if (!mbar_wait_warp(bars + C::B_RING_EMPTY + slot, at.ph ^ 1u, ab, 129)) { ok = false; break; }
+          if (i == 0) {  // the previous token's Q tiles have long been consumed
+            q_at[0] = lp[0];
+            q_at[1] = lp[1];
+          }
+          if (lane == 0) {
+            uint64_t* full = bars + C::B_RING_FULL + slot;
+            mbar_arrive_expect_tx(full, C::SLAB_TILE);
+            tma_load_3d(smem + C::OFF_RING + slot * C::SLAB_TILE, &tmQ, full, i * 64, 0, sg.tk);
+            for (int a = 0; a < C::NPROD / 2; ++a) mbar_arrive(full);
+          }
+          q_issued = i + 1;
+          __syncwarp();
+          at.step(1);
+        }
+        // the uses that the producers fill
+        for (int i = 0; ok && i < (sg.c1 - sg.c0) * (C::NLAT / 2); ++i) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int slot = g * C::NLST + lp[g].slot;
+            if (ok && !mbar_wait_warp(bars + C::B_RING_EMPTY + slot, lp[g].ph ^ 1u, ab, 124)) ok = false;
+            if (lane == 0 && ok) mbar_arrive(bars + C::B_RING_FULL + slot);
+            lp[g].step(1);
+          }
+        }
+      }
+      if (lane == 0 && ab.raised()) {
+        // aborted: Q tiles may still be landing; wait for the latest use of each slot (bounded, whatever the flag says)
+        int never = 0;
+        const AbortFlag no_abort{&never};
+        for (int i = 0; i < q_issued; ++i) {
+          RingPos<C::NLST>& w = (i & 1) ? q_at[1] : q_at[0];
+          if (i >= q_issued - 2 * C::NLST)
+            mbar_wait(bars + C::B_RING_FULL + (i & 1) * C::NLST + w.slot, w.ph, no_abort, 128);
+          w.step(1);
+        }
+      }
+    } else if (warp == C::W_MMA && rank == 0) {
+      // ---- score CTA's MMA warp: waits converged, one elected lane issues and commits ----
+      RingPos<C::NLST> lp[2];
+      RingPos<C::NRST> rp;
+      uint32_t sph = 1;
+      uint32_t qfree_ph = 1;
+      bool ok = true;
+      MlaSegIter segs = segs0;
+      MlaSeg sg;
+      while (ok && segs.next(sg)) {
+        // Q[tk] into TMEM once the previous piece's QK^T has read the old Q
+        if (!mbar_wait_warp(bars + C::B_Q_FREE, qfree_ph, ab, 132)) break;
+        qfree_ph ^= 1;
+        tc_fence_after();
+        for (int i = 0; i < MlaCfg::NSLAB_QK; ++i) {
+          RingPos<C::NLST>& at = (i & 1) ? lp[1] : lp[0];
+          const int slot = (i & 1) * C::NLST + at.slot;
+          if (!mbar_wait_warp(bars + C::B_RING_FULL + slot, at.ph, ab, 140)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t tile = ring + slot * C::SLAB_TILE;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_cp_128x256b(tmem + MlaCfg::Q_COL + (4 * i + kk) * 8, smem_desc(tile + kk * 32, 16, 1024, kSw128));
+            tc_commit(bars + C::B_RING_EMPTY + slot);
+            if (i == MlaCfg::NSLAB_QK - 1) tc_commit(bars + C::B_Q_IN);
+          }
+          __syncwarp();
+          at.step(1);
+        }
+        if (!ok) break;
+        for (int j = sg.c0; j < sg.c1 && ok; ++j) {
+          if (!mbar_wait_warp(bars + C::B_S_EMPTY, sph, ab, 134)) { ok = false; break; }
+          sph ^= 1;
+          tc_fence_after();
+          const uint32_t d = tmem + MlaCfg::S_COL;
+          for (int i = 0; i < C::NLAT; ++i) {
+            RingPos<C::NLST>& at = (i & 1) ? lp[1] : lp[0];
+            const int slot = (i & 1) * C::NLST + at.slot;
+            if (!mbar_wait_warp(bars + C::B_RING_FULL + slot, at.ph, ab, 133)) { ok = false; break; }
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t tile = ring + slot * C::SLAB_TILE;
+              const int slab = (i & 1) * 4 + (i >> 1);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_bf16_ts(d, tmem + MlaCfg::Q_COL + (4 * slab + kk) * 8, smem_desc(tile + kk * 32, 16, 1024, kSw128),
+                            MlaCfg::IDESC_QK, (i > 0 || kk > 0) ? 1u : 0u);
+              tc_commit(bars + C::B_RING_EMPTY + slot);
+            }
+            __syncwarp();
+            at.step(1);
+          }
+          if (!ok) break;
+          if (!mbar_wait_warp(bars + C::B_ROPE_FULL + rp.slot, rp.ph, ab, 135)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t tile = rope_ring + rp.slot * C::SLAB_TILE;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_ts(d, tmem + MlaCfg::Q_COL + (4 * C::NLAT + kk) * 8, smem_desc(tile + kk * 32, 16, 1024, kSw128),
+                          MlaCfg::IDESC_QK, 1u);
+            tc_commit(bars + C::B_ROPE_EMPTY + rp.slot);
+            tc_commit(bars + C::B_S_FULL);
+            if (j == sg.c1 - 1) tc_commit(bars + C::B_Q_FREE);
+          }
+          __syncwarp();
+          rp.step(1);
+        }
+      }
+    } else if (warp == C::W_MMA) {
+      // ---- value CTA's MMA warp ----
+      RingPos<C::NVST> vp;
+      int pb = 0;
+      uint32_t pph = 0;
+      int use = 0;  // messages consumed, to arm the receive barriers ahead
+      bool ok = true;
+      MlaSegIter segs = segs0;
+      MlaSeg sg;
+      while (ok && segs.next(sg)) {
+        for (int j = sg.c0; j < sg.c1 && ok; ++j) {
+          if (!mbar_wait_warp(bars + C::B_P_FULL + pb, pph, ab, 143)) { ok = false; break; }
+          const uint32_t any_rs =
+              reinterpret_cast<const volatile uint32_t*>(smem + C::OFF_MSG + pb * C::MSG_STRIDE + MlaCfg::MSG_CTRL)[0];
+          // A rescale needs O quiescent: commit everything issued so far to
+          // QUIESCE; the correction warps wait on it, rescale, then signal O_READY.
+          if (any_rs && j > sg.c0) {
+            if (elect_one()) tc_commit(bars + C::B_QUIESCE);
+            __syncwarp();
+          }
+          if (!mbar_wait_warp(bars + C::B_O_READY + pb, pph, ab, 144)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t pbase = msg + pb * C::MSG_STRIDE;
+          for (int u = 0; u < C::NK / C::VROWS; ++u) {
+            if (!mbar_wait_warp(bars + C::B_RING_FULL + vp.slot, vp.ph, ab, 142)) { ok = false; break; }
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t vbase = ring + vp.slot * C::V_TILE;
+#pragma unroll
+              for (int kk = 0; kk < C::VROWS / 16; ++kk) {
+                const int ko = u * C::VROWS + kk * 16;  // first key of this k-step within the chunk
+                const uint64_t ad = smem_desc(pbase + (ko >> 6) * 16384 + ((ko & 63) >> 4) * 32, 16, 1024, kSw128);
+#pragma unroll
+                for (int nh = 0; nh < 2; ++nh) {
+                  const uint64_t bd = smem_desc(vbase + nh * 4 * C::VSLAB + kk * 2048, C::VSLAB, 1024, kSw128);
+                  mma_bf16_ss(tmem + nh * 256, ad, bd, MlaCfg::IDESC_PV, (j > sg.c0 || u > 0 || kk > 0) ? 1u : 0u);
+                }
+              }
+              tc_commit(bars + C::B_RING_EMPTY + vp.slot);
+              if (u == C::NK / C::VROWS - 1) {
+                tc_commit_mc(bars + C::B_P_FREE + pb, 0x1);  // the score CTA's buffer pb is free
+                if (j == sg.c1 - 1) tc_commit(bars + C::B_PV_DONE);
+                const int nxt = use + C::NPB;  // re-arm this receive buffer for its next message
+                if (nxt < total_msgs) {
+                  const bool lastm = segs0.last_of_piece(nxt);
+                  mbar_arrive_expect_tx(bars + C::B_P_FULL + pb,
+                                        lastm ? MlaCfg::MSG_BYTES_LAST : MlaCfg::MSG_BYTES_MID);
+                }
+              }
+            }
+            __syncwarp();
+            vp.step(1);
+          }
+          if (!ok) break;
+          ++use;
+          if (++pb == C::NPB) { pb = 0; pph ^= 1; }
+        }
+      }
+    }
+  } else {
+    regs_up<C::REG_SM>();
+    const int quarter = static_cast<int>(warp & 3);
+    const int h = quarter * 32 + static_cast<int>(lane);  // thread = head row (TMEM lane)
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    if (rank == 0) {
+      // ---- softmax ----
+      const uint32_t peer_msg = map_to_peer(msg, 1);
+      const uint32_t peer_pfull = map_to_peer(smem_u32(bars + C::B_P_FULL), 1);
+      uint32_t sph = 0;
+      int pb = 0;
+      uint32_t pfree_ph = 1;
+      uint32_t stage_ph = 0;
+      bool ok = true;
+      int n = 0;
+      MlaSegIter segs = segs0;
+      MlaSeg sg;
+      for (; ok && segs.next(sg); ++n) {
+        const int ntk = segs.next_token();
+        if (h == 0 && ntk >= 0 && ntk != sg.tk) {
+          // warm L2 with the next piece's queries
+          const char* nq = reinterpret_cast<const char*>(p.q + static_cast<size_t>(ntk) * p.Hq * MlaCfg::D);
+          const uint32_t qbytes = static_cast<uint32_t>(p.Hq) * MlaCfg::D * 2;
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(nq), "r"(qbytes) : "memory");
+        }
+        float m_ref = -INFINITY;
+        float l_sum = 0.f;
+        const int mb = n & 1;
+        if (!mbar_wait(bars + C::B_MASK_FULL + mb, (n >> 1) & 1, ab, 139)) break;
+        const uint4* vm_tok = reinterpret_cast<const uint4*>(vmask_s + mb * (MlaCfg::KMAX / 32));
+        for (int j = sg.c0; j < sg.c1; ++j) {
+          const uint4 vm4 = vm_tok[j];
+          const uint32_t vmask[4] = {vm4.x, vm4.y, vm4.z, vm4.w};
+          if (!mbar_wait(bars + C::B_S_FULL, sph, ab, 136)) { ok = false; break; }
+          sph ^= 1;
+          tc_fence_after();
+          // this head's 128 scores into registers; the S buffer goes back to
+          // the tensor core at once
+          const uint32_t s_addr = tmem + lane_addr + MlaCfg::S_COL;
+          uint32_t sr[4][32];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) tmem_ld32_nowait(s_addr + g * 32, sr[g]);
+#pragma unroll
+          for (int g = 0; g < 4; ++g) tmem_ld_wait_fence(sr[g]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + C::B_S_EMPTY);
+          // absent rows score -inf (a chunk without any is the common case)
+          const bool all_valid = (vmask[0] & vmask[1] & vmask[2] & vmask[3]) == 0xffffffffu;
+          if (!all_valid) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!((vmask[g] >> c) & 1u)) sr[g][c] = 0xff800000u;
+          }
+          float mx[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            mx[g] = __uint_as_float(sr[g][0]);
+#pragma unroll
+            for (int c = 1; c < 32; ++c) mx[g] = fmaxf(mx[g], __uint_as_float(sr[g][c]));
+          }
+          float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+          // the reference maximum moves only by more than 2^8 (P <= 256), so O is rarely rescaled
+          float alpha = 1.f;
+          if (mc > -INFINITY && (m_ref == -INFINITY || mc > m_ref + 8.f)) {
+            alpha = (m_ref == -INFINITY) ? 0.f : exp2f(m_ref - mc);
+            m_ref = mc;
+            l_sum *= alpha;
+          }
+          const bool last = (j == sg.c1 - 1);
+          if (!mbar_wait(bars + C::B_P_FREE + pb, pfree_ph, ab, 137)) { ok = false; break; }
+          uint8_t* st = smem + C::OFF_MSG + pb * C::MSG_STRIDE;
+          // p = 2^(s scale log2e - m_ref) in bf16 into the swizzled P rows; the
+          // row sum takes the unrounded fp32 values in eight partial sums
+          const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
+          const float2 sl2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(neg_m, neg_m);
+          float2 part[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) part[i] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+#pragma unroll
+            for (int c4 = 0; c4 < 4; ++c4) {  // 8 keys = 16 bytes of the P row
+              uint32_t pk[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int c = c4 * 8 + 2 * i;
+                const float2 t = __ffma2_rn(make_float2(__uint_as_float(sr[g][c]), __uint_as_float(sr[g][c + 1])),
+                                            sl2, nm2);
+                const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+                pk[i] = pack_bf16x2(e.x, e.y);
+                part[i] = __fadd2_rn(part[i], e);
+              }
+              const int c8 = g * 4 + c4;
+              const int kslab = c8 >> 3, cc = c8 & 7;
+              *reinterpret_cast<uint4*>(st + kslab * 16384 + h * 128 + ((cc ^ (h & 7)) << 4)) =
+                  make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+          }
+          l_sum += ((part[0].x + part[0].y) + (part[1].x + part[1].y)) +
+                   ((part[2].x + part[2].y) + (part[3].x + part[3].y));
+          reinterpret_cast<float*>(st + MlaCfg::MSG_ALPHA)[h] = alpha;
+          const uint32_t any_rs = __ballot_sync(0xffffffffu, alpha != 1.f);
+          if (lane == 0 && any_rs) atomicOr(rescale_s + (pb & 1), 1);
+          if (last) {
+            reinterpret_cast<float*>(st + MlaCfg::MSG_L)[h] = l_sum;
+            reinterpret_cast<float*>(st + MlaCfg::MSG_M)[h] = m_ref;
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + C::B_STAGE);
+          if (warp == C::W_SM0 && lane == 0) {
+            if (!mbar_wait(bars + C::B_STAGE, stage_ph, ab, 138)) ok = false;
+            if (ok) {
+              uint32_t* ctrl = reinterpret_cast<uint32_t*>(st + MlaCfg::MSG_CTRL);
+              ctrl[0] = static_cast<uint32_t>(rescale_s[pb & 1]);
+              rescale_s[pb & 1] = 0;
+              fence_async_shared();
+              bulk_copy_to_peer(peer_msg + pb * C::MSG_STRIDE, smem_u32(st),
+                                last ? MlaCfg::MSG_BYTES_LAST : MlaCfg::MSG_BYTES_MID, peer_pfull + pb * 8);
+            }
+          }
+          stage_ph ^= 1;
+          if (++pb == C::NPB) { pb = 0; pfree_ph ^= 1; }
+          if (!ok) break;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + C::B_MASK_FREE + mb);
+      }
+    } else {
+      // ---- correction + epilogue ----
+      int pb = 0;
+      uint32_t pph = 0;
+      uint32_t pv_ph = 0;
+      uint32_t qz_ph = 0;
+      uint32_t epi_n = 0;  // staging tiles used by this warp (tile epi_n & 1 is next)
+      bool ok = true;
+      MlaSegIter segs = segs0;
+      MlaSeg sg;
+      while (ok && segs.next(sg)) {
+        const int tk = sg.tk;
+        float l_fin = 0.f, m_fin = -INFINITY;
+        for (int j = sg.c0; j < sg.c1; ++j) {
+          if (!mbar_wait(bars + C::B_P_FULL + pb, pph, ab, 145)) { ok = false; break; }
+          const uint8_t* mb = smem + C::OFF_MSG + pb * C::MSG_STRIDE;
+          const uint32_t any_rs = reinterpret_cast<const volatile uint32_t*>(mb + MlaCfg::MSG_CTRL)[0];
+          if (j == sg.c1 - 1) {
+            l_fin = reinterpret_cast<const float*>(mb + MlaCfg::MSG_L)[h];
+            m_fin = reinterpret_cast<const float*>(mb + MlaCfg::MSG_M)[h];
+          }
+          if (any_rs && j > sg.c0) {
+            const float alpha = reinterpret_cast<const float*>(mb + MlaCfg::MSG_ALPHA)[h];
+            if (!mbar_wait(bars + C::B_QUIESCE, qz_ph, ab, 146)) { ok = false; break; }
+            qz_ph ^= 1;
+            tc_fence_after();
+#pragma unroll 1
+            for (int cb = 0; cb < MlaCfg::DV / 32; ++cb) {
+              uint32_t r[32];
+              tmem_ld32(tmem + lane_addr + cb * 32, r);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * alpha);
+              tmem_st32(tmem + lane_addr + cb * 32, r);
+            }
+            tmem_st_wait();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + C::B_O_READY + pb);
+          if (++pb == C::NPB) { pb = 0; pph ^= 1; }
+        }
+        if (!ok) break;
+        if (!mbar_wait(bars + C::B_PV_DONE, pv_ph, ab, 147)) break;
+        pv_ph ^= 1;
+        tc_fence_after();
+        // the output leaves by bulk tensor stores from two 64-byte-swizzled
+        // staging tiles a warp: u = O / l in bf16 (32 values a tile), or a
+        // split piece's fp32 numerators (16 values a tile) and statistics
+        const bool partial = sg.slot >= 0;
+        const bool empty = !(l_fin > 0.f);
+        const float inv = partial ? 1.f : (empty ? 0.f : 1.f / l_fin);
+        uint8_t* stage = smem + C::OFF_EPI + quarter * 2 * C::EPI_TILE;
+        const uint32_t swz = (lane >> 1) & 3u;
+        auto emit = [&](const uint32_t (&w4)[4][4], int x) {
+          uint8_t* buf = stage + (epi_n & 1) * C::EPI_TILE;
+          if (lane == 0) bulk_wait_read_1();  // the store issued from this tile two tiles ago has read it
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(buf + lane * 64 + ((c ^ swz) << 4)) =
+                make_uint4(w4[c][0], w4[c][1], w4[c][2], w4[c][3]);
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            if (quarter * 32 < p.Hq) {
+              if (partial) tma_store_3d(&tmP, buf, x, quarter * 32, sg.slot);
+              else tma_store_3d(&tmO, buf, x, quarter * 32, tk);
+            }
+            bulk_commit();
+          }
+          ++epi_n;
+        };
+        auto store_block = [&](int cb, const uint32_t (&r)[32]) {
+          uint32_t w4[4][4];
+          if (partial) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w4[c][e] = r[16 * hf + 4 * c + e];
+              emit(w4, cb * 32 + 16 * hf);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w4[c][e] = pack_bf16x2(__uint_as_float(r[8 * c + 2 * e]) * inv, __uint_as_float(r[8 * c + 2 * e + 1]) * inv);
+            emit(w4, cb * 32);
+          }
+        };
+        uint32_t ra[32], rb[32];
+        tmem_ld32_nowait(tmem + lane_addr, ra);
+        tmem_ld_wait_fence(ra);
+#pragma unroll 1
+        for (int cb = 0; cb < MlaCfg::DV / 32; cb += 2) {
+          tmem_ld32_nowait(tmem + lane_addr + (cb + 1) * 32, rb);
+          store_block(cb, ra);
+          tmem_ld_wait_fence(rb);
+          if (cb + 2 < MlaCfg::DV / 32) tmem_ld32_nowait(tmem + lane_addr + (cb + 2) * 32, ra);
+          store_block(cb + 1, rb);
+          if (cb + 2 < MlaCfg::DV / 32) tmem_ld_wait_fence(ra);
+        }
+        if (h < p.Hq) {
+          if (partial) {
+            float* part = p.part + static_cast<size_t>(sg.slot) * kMlaPartFloats;
+            part[128 * MlaCfg::DV + h] = m_fin;
+            part[128 * MlaCfg::DV + 128 + h] = l_fin;
+          } else if (p.lse) {
+            p.lse[static_cast<size_t>(tk) * p.Hq + h] =
+                empty ? -INFINITY : (m_fin + log2f(l_fin)) * 0.69314718055994531f;
+          }
+        }
+        tc_fence_before();
+      }
+      if (lane == 0) bulk_wait_all();  // the output stores have completed before the CTA leaves
+    }
+  }
+
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == C::W_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace dsa

@@ -262,3 +262,68 @@ def rope_quantize_e4m3(x, pos, *, rope_dim: int = 64, base: float = 10000.0, int
     shape = r.shape
     codes, scale = quantize_e4m3(r.reshape(shape[0], -1).astype(np.float32))
     return codes.reshape(shape), scale
+
+
+# ---------------------------------------------------------------------------
+# The 4-bit latent cache (row format in include/dsa.h) and the root-mean-square
+# norm, from their definitions in float64. Serving layout of this library, no
+# counterpart in the pages.
+# ---------------------------------------------------------------------------
+Q4_ROW_BYTES = 416
+_Q4_STEPS = np.array([(8 + b % 8) * 2.0 ** (b // 8 - 21) for b in range(256)])  # a scale byte's value
+
+
+def _bf16_from_f32(x: np.ndarray) -> np.ndarray:
+    """bf16 bits of fp32 values, to nearest with ties to even; a NaN stays one."""
+    u = np.ascontiguousarray(x, dtype=np.float32).view(np.uint32).astype(np.uint64)
+    r = ((u + 0x7FFF + ((u >> 16) & 1)) >> 16).astype(np.uint16)
+    return np.where(np.isnan(x), np.uint16(0x7FC0), r)
+
+
+def q4_quantize(x) -> np.ndarray:
+    """Rows x [n, 576] (values exact in fp32) as [n, 416] bytes of the 4-bit cache."""
+    x = np.asarray(x, dtype=np.float64)
+    n = x.shape[0]
+    g = x[:, :512].reshape(n, 32, 16)
+    g = np.where(np.isnan(g), 0.0, g)
+    amax = np.abs(g).max(axis=2)
+    b = np.minimum(np.searchsorted(7 * _Q4_STEPS, amax, side="left"), 255)
+    q = np.clip(np.rint(g / _Q4_STEPS[b][:, :, None]), -7, 7).astype(np.int64) + 8
+    w = np.zeros((n, 64), dtype=np.uint32)
+    v = q.reshape(n, 64, 8)
+    for j in range(8):
+        w |= v[:, :, j].astype(np.uint32) << np.uint32(4 * (j // 2 + 4 * (j % 2)))
+    out = np.empty((n, Q4_ROW_BYTES), dtype=np.uint8)
+    out[:, :256] = w.view(np.uint8).reshape(n, 256)
+    out[:, 256:288] = b
+    out[:, 288:] = _bf16_from_f32(x[:, 512:].astype(np.float32)).view(np.uint8).reshape(n, 128)
+    return out
+
+
+def q4_values(rows) -> np.ndarray:
+    """The values [n, 576] in float64 that rows [n, 416] of the 4-bit cache stand for."""
+    b = np.ascontiguousarray(_np(rows, np.uint8))
+    n = b.shape[0]
+    w = np.ascontiguousarray(b[:, :256]).view(np.uint32).reshape(n, 64, 1)
+    shift = np.array([4 * (j // 2 + 4 * (j % 2)) for j in range(8)], dtype=np.uint32)
+    c = ((w >> shift) & np.uint32(15)).astype(np.float64) - 8.0
+    lat = c.reshape(n, 32, 16) * _Q4_STEPS[b[:, 256:288]][:, :, None]
+    rope = bf16_to_f64(np.ascontiguousarray(b[:, 288:]).view(np.uint16))
+    return np.concatenate([lat.reshape(n, 512), rope], axis=1)
+
+
+def rms_norm(x, weight=None, residual=None, eps: float = 1e-6):
+    """(h, y) in float64: h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight."""
+    h = np.asarray(x, dtype=np.float64)
+    if residual is not None:
+        h = h + np.asarray(residual, dtype=np.float64)
+    y = h / np.sqrt(np.mean(h * h, axis=1, keepdims=True) + eps)
+    return h, (y if weight is None else y * np.asarray(weight, dtype=np.float64))
+
+
+def e4m3_nearest(v) -> np.ndarray:
+    """The E4M3 values nearest to v (float64), ties to even, saturating at 448."""
+    v = np.asarray(v, dtype=np.float64)
+    e = np.frexp(np.maximum(np.abs(v), 2.0 ** -6))[1] - 1
+    step = np.ldexp(1.0, e - 3)
+    return np.clip(np.rint(v / step) * step, -448.0, 448.0)
