@@ -11,24 +11,30 @@
 // in TMEM, computes S = Q C^T for 128 rows at a time and the softmax, and
 // sends P to the value CTA, which accumulates O += P V in its whole TMEM. New
 // here is how the operand tiles come about:
-//   * Eight producer warps in each CTA load codes and scales straight into
-//     registers, one whole chunk ahead of their use (a register set is
-//     reloaded with the next chunk's bytes as soon as it has been expanded),
-//     expand them to bf16 and store them into the swizzled tiles that the MMA
-//     reads. One thread takes the 64 values of one row in one slab: 32
-//     contiguous bytes of codes in one load, eight 16-byte stores that fall
-//     into eight different bank groups for eight neighbouring rows.
-//   * The latent slabs of a chunk go through two rings of three tiles, each
+//   * Eight producer warps in each CTA copy codes and scales as they are
+//     (cp.async) into a queue in shared memory, one chunk ahead of their use,
+//     then expand them to bf16 and store them into the swizzled tiles that the
+//     MMA reads. One thread takes the 64 values of one row in one slab, for
+//     the copy as for the expansion, so its queue is its own and needs no
+//     barrier; its eight 16-byte stores fall into eight different bank groups
+//     for eight neighbouring rows. The loop is kept short on purpose: with the
+//     queue in registers it has to be unrolled over a chunk, and the code of
+//     all roles together then runs out of the instruction caches (measured: a
+//     quarter of all warp time waiting for instructions, 5.8 us a chunk).
+//   * The latent slabs of a chunk go through two rings of two tiles, each
 //     filled by four of the warps (slabs 0-3 and 4-7); the rotary slab (bf16 as
-//     it stands) has two tiles of its own. Q's tiles pass through both rings.
-//     A parity tells a phase only from its neighbours, so nobody may be two
-//     uses of a slot ahead or behind: the warp that loads Q also takes part in
-//     filling every other tile (one arrival, after it has seen the slot free),
-//     and the producers pass over Q's uses only once a barrier of its own says
-//     that Q is in TMEM.
+//     it stands) is copied straight into two tiles of its own. Q's tiles pass
+//     through both rings. A parity tells a phase only from its neighbours, so
+//     nobody may be two uses of a slot ahead or behind: the warp that loads Q
+//     also takes part in filling every other tile (one arrival, after it has
+//     seen the slot free), and the producers pass over Q's uses only once a
+//     barrier of its own says that Q is in TMEM.
 //   * Page lookups and range checks are made once a token, when the index row
 //     is staged: the row numbers in shared memory are final (-1 for absent).
-//     Absent rows are expanded from code 8, which is zero at any scale.
+//     Absent rows are copied as zero bytes, which stand for finite values,
+//     and get probability 0.
+//   * The stores reach the tensor core's proxy by a fence on the MMA warp's
+//     side, between its wait for a tile and the first MMA on it.
 //   * Sixteen warps do not fit the softmax's registers at an even share, so
 //     the warp groups trade registers at the start.
 #pragma once
@@ -43,30 +49,39 @@ struct MlaQ4Cfg {
   static constexpr int NK = MlaCfg::NK;
   static constexpr int SLAB_TILE = MlaCfg::SLAB_TILE;  // 128 rows x 128 bytes
   static constexpr int NLAT = 8;                       // latent slabs of 64 values
-  static constexpr int NLST = 3;                       // tiles of each of the two latent rings (score CTA)
+  static constexpr int NLST = 2;                       // tiles of each of the two latent rings (score CTA)
   static constexpr int NRST = 2;                       // rotary tiles (score CTA)
   static constexpr int VROWS = MlaCfg::VROWS;
   static constexpr int VSLAB = MlaCfg::VSLAB;
   static constexpr int V_TILE = MlaCfg::V_TILE;
-  static constexpr int NVST = 4;                       // value sub-tile ring (value CTA)
+  static constexpr int NVST = 3;                       // value sub-tile ring (value CTA)
   static constexpr int NPB = MlaCfg::NPB;
   static constexpr int NPROD = 8;                      // producer warps
   static constexpr int W_SM0 = 8;                      // four softmax / epilogue warps
   static constexpr int W_MMA = 12;
   static constexpr int W_Q = 13;                       // loads Q's tiles (score CTA)
   static constexpr int NTHREADS = 16 * 32;
-  // registers a thread after the trade: 2 * 112 + 208 + 72 <= 4 * 128
-  static constexpr int REG_PROD = 112, REG_SM = 208, REG_MMA = 72;
+  // registers a thread after the trade: 2 * 96 + 208 + 80 <= 4 * 128
+  static constexpr int REG_PROD = 96, REG_SM = 208, REG_MMA = 80;
   static constexpr int OFF_RING = 0;
   static constexpr int OFF_ROPE = 2 * NLST * SLAB_TILE;  // score CTA
   static constexpr int RING_BYTES = (2 * NLST + NRST) * SLAB_TILE;
-  static_assert(RING_BYTES >= NVST * V_TILE, "the value ring shares the space");
+  static_assert(RING_BYTES == NVST * V_TILE, "the value ring takes the same space");
+  // The producers' queues: 4 entries of 32 bytes of codes a thread, in pieces
+  // of 16 bytes (piece i of thread t at (i * 256 + t) * 16). The scales: 4
+  // bytes an entry in the value CTA; 16 bytes a chunk, two chunks, in the
+  // score CTA, which has no use for the output staging.
+  static constexpr int NQ = 4;
+  static constexpr int OFF_FIFO = OFF_RING + RING_BYTES;
+  static constexpr int OFF_VSC = OFF_FIFO + NQ * 2 * NPROD * 32 * 16;
   static constexpr int MSG_STRIDE = MlaCfg::MSG_STRIDE;
-  static constexpr int OFF_MSG = OFF_RING + RING_BYTES;
+  static constexpr int OFF_MSG = OFF_VSC + NQ * NPROD * 32 * 4;
   static constexpr int OFF_IDX = OFF_MSG + NPB * MSG_STRIDE;
   static constexpr int OFF_VMASK = OFF_IDX + MlaCfg::KMAX * 4;  // u32 [2][KMAX / 32]
   static constexpr int OFF_EPI = (OFF_VMASK + 2 * (MlaCfg::KMAX / 32) * 4 + 1023) / 1024 * 1024;
   static constexpr int EPI_TILE = MlaCfg::EPI_TILE;
+  static constexpr int OFF_SSC = OFF_EPI;
+  static_assert(2 * NPROD * 32 * 16 <= 4 * 2 * EPI_TILE, "the score CTA's scales");
   static constexpr int OFF_BAR = OFF_EPI + 4 * 2 * EPI_TILE;
   // barriers (the same offsets in both CTAs)
   static constexpr int NRING = 2 * NLST;                  // score: ring g's slots from g * NLST; value: [NVST] sub-tiles
@@ -130,30 +145,45 @@ __device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&v)[4]) {
                : "memory");
 }
 
-// 64 values of a row (8 words of codes, 4 scale bytes) into its 128 bytes of a
-// swizzled tile: 16-byte piece c goes to c ^ (row & 7).
-__device__ __forceinline__ void expand_row(uint32_t row_addr, uint32_t swz, const uint32_t (&codes)[8],
-                                           uint32_t scales) {
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const uint32_t s2 = q4_scale_pair((scales >> (8 * g)) & 0xffu);
-    const uint32_t off2 = q4_offset_pair(s2);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t v[4];
-      q4_values(codes[2 * g + h], s2, off2, v);
-      sts128(row_addr + (static_cast<uint32_t>((2 * g + h) << 4) ^ swz), v);
-    }
-  }
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cp_async_4_zfill(uint32_t dst, const void* src, bool valid) {
+  const uint32_t n = valid ? 4u : 0u;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// A row's 32 bytes at `off`, or codes of zero for an absent row.
-__device__ __forceinline__ void load_codes(uint32_t (&r)[8], const uint8_t* row, int off) {
-  if (row) {
-    ldg256(row + off, r);
-  } else {
+// 64 values of a row (two 16-byte pieces of codes `step` bytes apart, 4 scale
+// bytes) into its 128 bytes of a swizzled tile: piece c goes to c ^ (row & 7).
+__device__ __forceinline__ void expand_row(uint32_t row_addr, uint32_t swz, uint32_t codes, uint32_t step,
+                                           uint32_t scales) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) r[k] = 0x88888888u;
+  for (int h = 0; h < 2; ++h) {
+    const uint4 w4 = lds128(codes + h * step);
+    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t s2 = q4_scale_pair((scales >> (8 * (2 * h + (i >> 1)))) & 0xffu);
+      const uint32_t off2 = q4_offset_pair(s2);
+      uint32_t v[4];
+      q4_values(w[i], s2, off2, v);
+      sts128(row_addr + (static_cast<uint32_t>((4 * h + i) << 4) ^ swz), v);
+    }
   }
 }
 
@@ -250,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
       mbar_init(bars + C::B_RING_EMPTY + i, 1);
     }
     for (int i = 0; i < C::NRST; ++i) {
-      mbar_init(bars + C::B_ROPE_FULL + i, C::NPROD);
+      mbar_init(bars + C::B_ROPE_FULL + i, C::NPROD * 32);
       mbar_init(bars + C::B_ROPE_EMPTY + i, 1);
     }
     mbar_init(bars + C::B_S_FULL, 1);
@@ -307,6 +337,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
       uint64_t* lempty = bars + C::B_RING_EMPTY + grp * C::NLST;
       const uint32_t lring = ring + grp * C::NLST * C::SLAB_TILE + r * 128;
       RingPos<C::NRST> rp;
+      constexpr uint32_t kQueue = C::NPROD * 32 * 16;
+      const uint32_t codes_q = smem_u32(smem + C::OFF_FIFO) + ptid * 16, sc_q = smem_u32(smem + C::OFF_SSC) + ptid * 16;
       int n = 0;
       bool ok = true;
       for (; ok && segs.next(sg); ++n) {
@@ -320,68 +352,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
                                    bars + C::B_PSTAGE, stage_ph, ab))
           break;
         if (lane == 0) mbar_arrive(bars + C::B_MASK_FULL + mb);
-        auto row_of = [&](int j) -> const uint8_t* {
-          const int row = idx_s[j * C::NK + r];
-          return row >= 0 ? base + static_cast<long long>(row) * kQ4RowBytes : nullptr;
+        // copies of chunk j: this thread's row (codes of one slab an entry,
+        // the group's 16 scale bytes with the first) and its rotary pieces
+        const uint8_t* row = nullptr;
+        auto copy_codes = [&](int j, int i) {
+          if (i == 0) {
+            const int rn = idx_s[j * C::NK + r];
+            row = rn >= 0 ? base + static_cast<long long>(rn) * kQ4RowBytes : nullptr;
+            cp_async_16_zfill(sc_q + (j & 1) * kQueue, (row ? row : p.cache) + kQ4Scales + 16 * grp, row != nullptr);
+          }
+          const uint8_t* src = (row ? row : p.cache) + (4 * grp + i) * 32;
+          cp_async_16_zfill(codes_q + (2 * i) * kQueue, src, row != nullptr);
+          cp_async_16_zfill(codes_q + (2 * i + 1) * kQueue, src + 16, row != nullptr);
         };
-        uint32_t codes[4][8];
-        uint4 sc, rope[4];
-        auto load_scales = [&](const uint8_t* row) {
-          return row ? ldg128(row + kQ4Scales + 16 * grp) : make_uint4(0, 0, 0, 0);
-        };
-        auto load_rope = [&](int j) {
+        auto copy_rope = [&](int j) {
+          const uint32_t rt = rope_ring + rp.slot * C::SLAB_TILE + rr * 128 + ((rc ^ (rr & 7)) << 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int row = idx_s[j * C::NK + rr + 32 * k];
-            rope[k] = row >= 0 ? ldg128(base + static_cast<long long>(row) * kQ4RowBytes + kQ4Rope + 16 * rc)
-                               : make_uint4(0, 0, 0, 0);
+            const int rn = idx_s[j * C::NK + rr + 32 * k];
+            const uint8_t* src = rn >= 0 ? base + static_cast<long long>(rn) * kQ4RowBytes : p.cache;
+            cp_async_16_zfill(rt + k * 32 * 128, src + kQ4Rope + 16 * rc, rn >= 0);
           }
+          cp_async_mbar_arrive(bars + C::B_ROPE_FULL + rp.slot);
+          rp.step(1);
         };
-        {
-          const uint8_t* row = row_of(sg.c0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) load_codes(codes[i], row, (4 * grp + i) * 32);
-          sc = load_scales(row);
-          load_rope(sg.c0);
+        // the first chunk's copies, one group an entry
+        if (!mbar_wait(bars + C::B_ROPE_EMPTY + rp.slot, rp.ph ^ 1u, ab, 132)) break;
+        copy_rope(sg.c0);
+#pragma unroll 1
+        for (int i = 0; i < C::NQ; ++i) {
+          copy_codes(sg.c0, i);
+          cp_async_commit();
         }
         // Q's tiles go first (five through ring 0, four through ring 1)
         if (!mbar_wait(bars + C::B_Q_IN, n & 1, ab, 125)) break;
         lp.step((MlaCfg::NSLAB_QK + 1 - grp) / 2);
-        for (int j = sg.c0; j < sg.c1; ++j) {
-          const bool more = j + 1 < sg.c1;
-          // rotary tile
-          if (!mbar_wait(bars + C::B_ROPE_EMPTY + rp.slot, rp.ph ^ 1u, ab, 132)) { ok = false; break; }
-          const uint32_t rt = rope_ring + rp.slot * C::SLAB_TILE;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int row = rr + 32 * k;
-            const uint32_t v[4] = {rope[k].x, rope[k].y, rope[k].z, rope[k].w};
-            sts128(rt + row * 128 + ((rc ^ (row & 7)) << 4), v);
-          }
-          fence_async_shared();
+#pragma unroll 1
+        for (int k = 4 * sg.c0; k < 4 * sg.c1; ++k) {
+          const int j = k >> 2, i = k & 3;
+          cp_async_wait<C::NQ - 1>();  // this entry has landed
+          if (!mbar_wait(lempty + lp.slot, lp.ph ^ 1u, ab, 131)) { ok = false; break; }
+          expand_row(lring + lp.slot * C::SLAB_TILE, swz, codes_q + 2 * i * kQueue, kQueue,
+                     lds32(sc_q + (j & 1) * kQueue + 4 * i));
           __syncwarp();
-          if (lane == 0) mbar_arrive(bars + C::B_ROPE_FULL + rp.slot);
-          rp.step(1);
-          const uint8_t* nrow = nullptr;
-          uint4 sc_next = make_uint4(0, 0, 0, 0);
-          if (more) {
-            load_rope(j + 1);
-            nrow = row_of(j + 1);
-            sc_next = load_scales(nrow);
+          if (lane == 0) mbar_arrive(lfull + lp.slot);
+          lp.step(1);
+          if (j + 1 < sg.c1) {
+            copy_codes(j + 1, i);
+            if (i == 3) {
+              // the slot's last use was two chunks back: over, since this chunk's first tiles have been read
+              if (!mbar_wait(bars + C::B_ROPE_EMPTY + rp.slot, rp.ph ^ 1u, ab, 132)) { ok = false; break; }
+              copy_rope(j + 1);
+            }
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (!mbar_wait(lempty + lp.slot, lp.ph ^ 1u, ab, 131)) { ok = false; break; }
-            const uint32_t s4 = i == 0 ? sc.x : i == 1 ? sc.y : i == 2 ? sc.z : sc.w;
-            expand_row(lring + lp.slot * C::SLAB_TILE, swz, codes[i], s4);
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(lfull + lp.slot);
-            if (more) load_codes(codes[i], nrow, (4 * grp + i) * 32);
-            lp.step(1);
-          }
-          if (!ok) break;
-          sc = sc_next;
+          cp_async_commit();
         }
       }
     } else {
@@ -389,6 +413,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
       const uint32_t swz = (lane & 7u) << 4;
       const uint32_t row_off = warp * C::VSLAB + lane * 128;
       RingPos<C::NVST> vp;
+      constexpr uint32_t kQueue = C::NPROD * 32 * 16;
+      const uint32_t codes_q = smem_u32(smem + C::OFF_FIFO) + ptid * 16, sc_q = smem_u32(smem + C::OFF_VSC) + ptid * 4;
       bool ok = true;
       while (ok && segs.next(sg)) {
         long long first;
@@ -398,29 +424,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
         if (!stage_rows_q4<kPaged>(idx_s, nullptr, p, sg.tk, nchunk * C::NK, trows, ptid, bars + C::B_PSTAGE,
                                    stage_ph, ab))
           break;
-        uint32_t codes[4][8], sc[4];
-        auto load_sub = [&](int j, int u) {
-          const int row = idx_s[j * C::NK + u * C::VROWS + static_cast<int>(lane)];
-          const uint8_t* rp = row >= 0 ? base + static_cast<long long>(row) * kQ4RowBytes : nullptr;
-          load_codes(codes[u], rp, static_cast<int>(warp) * 32);
-          sc[u] = rp ? ldg32(rp + kQ4Scales + 4 * warp) : 0u;
+        auto copy_sub = [&](int k) {  // entry k: rows 32 k .. of the selection
+          const int rn = idx_s[k * C::VROWS + static_cast<int>(lane)];
+          const uint8_t* row = rn >= 0 ? base + static_cast<long long>(rn) * kQ4RowBytes : p.cache;
+          const int i = k & 3;
+          cp_async_16_zfill(codes_q + (2 * i) * kQueue, row + warp * 32, rn >= 0);
+          cp_async_16_zfill(codes_q + (2 * i + 1) * kQueue, row + warp * 32 + 16, rn >= 0);
+          cp_async_4_zfill(sc_q + i * (kQueue / 4), row + kQ4Scales + 4 * warp, rn >= 0);
         };
-#pragma unroll
-        for (int u = 0; u < 4; ++u) load_sub(sg.c0, u);
-        for (int j = sg.c0; ok && j < sg.c1; ++j) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            if (!mbar_wait(bars + C::B_RING_EMPTY + vp.slot, vp.ph ^ 1u, ab, 141)) { ok = false; break; }
-            expand_row(ring + vp.slot * C::V_TILE + row_off, swz, codes[u], sc[u]);
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars + C::B_RING_FULL + vp.slot);
-            if (j + 1 < sg.c1) load_sub(j + 1, u);
-            vp.step(1);
-          }
+#pragma unroll 1
+        for (int i = 0; i < C::NQ; ++i) {
+          copy_sub(4 * sg.c0 + i);
+          cp_async_commit();
+        }
+#pragma unroll 1
+        for (int k = 4 * sg.c0; k < 4 * sg.c1; ++k) {
+          const int i = k & 3;
+          cp_async_wait<C::NQ - 1>();
+          if (!mbar_wait(bars + C::B_RING_EMPTY + vp.slot, vp.ph ^ 1u, ab, 141)) { ok = false; break; }
+          expand_row(ring + vp.slot * C::V_TILE + row_off, swz, codes_q + 2 * i * kQueue, kQueue,
+                     lds32(sc_q + i * (kQueue / 4)));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + C::B_RING_FULL + vp.slot);
+          if (k + C::NQ < 4 * sg.c1) copy_sub(k + C::NQ);
+          cp_async_commit();
+          vp.step(1);
         }
       }
     }
+    cp_async_wait<0>();
   } else if (warp >= C::W_MMA) {
     regs_down<C::REG_MMA>();
     if (warp == C::W_Q && rank == 0) {
@@ -514,6 +546,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
             if (!mbar_wait_warp(bars + C::B_RING_FULL + slot, at.ph, ab, 133)) { ok = false; break; }
             tc_fence_after();
             if (elect_one()) {
+              fence_async_shared();
               const uint32_t tile = ring + slot * C::SLAB_TILE;
               const int slab = (i & 1) * 4 + (i >> 1);
 #pragma unroll
@@ -529,6 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
           if (!mbar_wait_warp(bars + C::B_ROPE_FULL + rp.slot, rp.ph, ab, 135)) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) {
+            fence_async_shared();
             const uint32_t tile = rope_ring + rp.slot * C::SLAB_TILE;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
@@ -569,6 +603,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
             if (!mbar_wait_warp(bars + C::B_RING_FULL + vp.slot, vp.ph, ab, 142)) { ok = false; break; }
             tc_fence_after();
             if (elect_one()) {
+              fence_async_shared();
               const uint32_t vbase = ring + vp.slot * C::V_TILE;
 #pragma unroll
               for (int kk = 0; kk < C::VROWS / 16; ++kk) {
