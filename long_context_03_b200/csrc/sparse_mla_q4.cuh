@@ -21,14 +21,19 @@
 //     queue in registers it has to be unrolled over a chunk, and the code of
 //     all roles together then runs out of the instruction caches (measured: a
 //     quarter of all warp time waiting for instructions, 5.8 us a chunk).
-//   * The latent slabs of a chunk go through two rings of two tiles, each
-//     filled by four of the warps (slabs 0-3 and 4-7); the rotary slab (bf16 as
-//     it stands) is copied straight into two tiles of its own. Q's tiles pass
-//     through both rings. A parity tells a phase only from its neighbours, so
-//     nobody may be two uses of a slot ahead or behind: the warp that loads Q
-//     also takes part in filling every other tile (one arrival, after it has
-//     seen the slot free), and the producers pass over Q's uses only once a
-//     barrier of its own says that Q is in TMEM.
+//   * The latent slabs of a chunk go through two stages of two tiles (slabs i
+//     and 4 + i, each filled by four of the warps): one wait, one proxy fence
+//     and one commit serve eight MMAs, whose 512 cycles cover what the issuing
+//     warp spends on them. With a wait for each tile it could not keep up (577
+//     cycles for 256 of MMA). The rotary slab (bf16 as it stands) is copied
+//     straight into two tiles of its own. Q's tiles pass through the stages
+//     too, in six uses (the sixth is empty), so that the uses of a stage and
+//     with them its parities are the same for every chunk of a token. A parity
+//     tells a phase only from its neighbours, so nobody may be two uses of a
+//     stage ahead or behind: the warp that loads Q also takes part in filling
+//     every other use (one arrival, after it has seen the stage free), and the
+//     producers pass over Q's uses only once a barrier of its own says that Q
+//     is in TMEM.
 //   * Page lookups and range checks are made once a token, when the index row
 //     is staged: the row numbers in shared memory are final (-1 for absent).
 //     Absent rows are copied as zero bytes, which stand for finite values,
@@ -49,7 +54,9 @@ struct MlaQ4Cfg {
   static constexpr int NK = MlaCfg::NK;
   static constexpr int SLAB_TILE = MlaCfg::SLAB_TILE;  // 128 rows x 128 bytes
   static constexpr int NLAT = 8;                       // latent slabs of 64 values
-  static constexpr int NLST = 2;                       // tiles of each of the two latent rings (score CTA)
+  static constexpr int NST = 2;                        // latent stages of two tiles (score CTA)
+  static constexpr int STAGE = 2 * SLAB_TILE;
+  static constexpr int Q_USES = 6;                     // stage uses of a token's Q tiles
   static constexpr int NRST = 2;                       // rotary tiles (score CTA)
   static constexpr int VROWS = MlaCfg::VROWS;
   static constexpr int VSLAB = MlaCfg::VSLAB;
@@ -64,8 +71,8 @@ struct MlaQ4Cfg {
   // registers a thread after the trade: 2 * 96 + 208 + 80 <= 4 * 128
   static constexpr int REG_PROD = 96, REG_SM = 208, REG_MMA = 80;
   static constexpr int OFF_RING = 0;
-  static constexpr int OFF_ROPE = 2 * NLST * SLAB_TILE;  // score CTA
-  static constexpr int RING_BYTES = (2 * NLST + NRST) * SLAB_TILE;
+  static constexpr int OFF_ROPE = NST * STAGE;         // score CTA
+  static constexpr int RING_BYTES = NST * STAGE + NRST * SLAB_TILE;
   static_assert(RING_BYTES == NVST * V_TILE, "the value ring takes the same space");
   // The producers' queues: 4 entries of 32 bytes of codes a thread, in pieces
   // of 16 bytes (piece i of thread t at (i * 256 + t) * 16). The scales: 4
@@ -84,8 +91,7 @@ struct MlaQ4Cfg {
   static_assert(2 * NPROD * 32 * 16 <= 4 * 2 * EPI_TILE, "the score CTA's scales");
   static constexpr int OFF_BAR = OFF_EPI + 4 * 2 * EPI_TILE;
   // barriers (the same offsets in both CTAs)
-  static constexpr int NRING = 2 * NLST;                  // score: ring g's slots from g * NLST; value: [NVST] sub-tiles
-  static_assert(NRING >= NVST, "one set of barriers serves both CTAs");
+  static constexpr int NRING = NST > NVST ? NST : NVST;   // score: [NST] stages; value: [NVST] sub-tiles
   static constexpr int B_RING_FULL = 0;
   static constexpr int B_RING_EMPTY = B_RING_FULL + NRING;
   static constexpr int B_ROPE_FULL = B_RING_EMPTY + NRING;  // [NRST]
@@ -275,8 +281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
     rescale_s[0] = 0;
     rescale_s[1] = 0;
     for (int i = 0; i < C::NRING; ++i) {
-      // arrivals: four producer warps and Q's a latent tile, eight a value sub-tile
-      mbar_init(bars + C::B_RING_FULL + i, rank == 0 ? C::NPROD / 2 + 1 : C::NPROD);
+      mbar_init(bars + C::B_RING_FULL + i, rank == 0 ? C::NPROD + 1 : C::NPROD);  // the producer warps, and Q's
       mbar_init(bars + C::B_RING_EMPTY + i, 1);
     }
     for (int i = 0; i < C::NRST; ++i) {
@@ -315,7 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
   cluster_sync_all();
   griddep_wait();  // nothing of global memory is touched before
   tc_fence_after();
-  const uint32_t tmem = *tmem_base_s;
+  constexpr uint32_t tmem = 0;  // the CTA holds all 512 columns, so they start at 0
   const uint32_t ring = smem_u32(smem + C::OFF_RING);
   const uint32_t rope_ring = smem_u32(smem + C::OFF_ROPE);
   const uint32_t msg = smem_u32(smem + C::OFF_MSG);
@@ -332,10 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
       const int r = ptid & 127;
       const uint32_t swz = static_cast<uint32_t>(r & 7) << 4;
       const int rc = ptid & 7, rr = ptid >> 3;  // rotary: piece rc of rows rr + 32 k
-      RingPos<C::NLST> lp;  // of this group's ring
-      uint64_t* lfull = bars + C::B_RING_FULL + grp * C::NLST;
-      uint64_t* lempty = bars + C::B_RING_EMPTY + grp * C::NLST;
-      const uint32_t lring = ring + grp * C::NLST * C::SLAB_TILE + r * 128;
+      const uint32_t ltile = ring + grp * C::SLAB_TILE + r * 128;
       RingPos<C::NRST> rp;
       constexpr uint32_t kQueue = C::NPROD * 32 * 16;
       const uint32_t codes_q = smem_u32(smem + C::OFF_FIFO) + ptid * 16, sc_q = smem_u32(smem + C::OFF_SSC) + ptid * 16;
@@ -384,19 +386,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
           copy_codes(sg.c0, i);
           cp_async_commit();
         }
-        // Q's tiles go first (five through ring 0, four through ring 1)
-        if (!mbar_wait(bars + C::B_Q_IN, n & 1, ab, 125)) break;
-        lp.step((MlaCfg::NSLAB_QK + 1 - grp) / 2);
+        if (!mbar_wait(bars + C::B_Q_IN, n & 1, ab, 125)) break;  // Q's tiles go first
+        // parity of a stage's first use in a chunk: three uses a token by Q, two a chunk
+        const uint32_t par = static_cast<uint32_t>(n & 1) ^ 1u;
 #pragma unroll 1
         for (int k = 4 * sg.c0; k < 4 * sg.c1; ++k) {
           const int j = k >> 2, i = k & 3;
           cp_async_wait<C::NQ - 1>();  // this entry has landed
-          if (!mbar_wait(lempty + lp.slot, lp.ph ^ 1u, ab, 131)) { ok = false; break; }
-          expand_row(lring + lp.slot * C::SLAB_TILE, swz, codes_q + 2 * i * kQueue, kQueue,
+          if (!mbar_wait(bars + C::B_RING_EMPTY + (i & 1), par ^ static_cast<uint32_t>(i >> 1) ^ 1u, ab, 131)) {
+            ok = false;
+            break;
+          }
+          expand_row(ltile + (i & 1) * C::STAGE, swz, codes_q + 2 * i * kQueue, kQueue,
                      lds32(sc_q + (j & 1) * kQueue + 4 * i));
           __syncwarp();
-          if (lane == 0) mbar_arrive(lfull + lp.slot);
-          lp.step(1);
+          if (lane == 0) mbar_arrive(bars + C::B_RING_FULL + (i & 1));
           if (j + 1 < sg.c1) {
             copy_codes(j + 1, i);
             if (i == 3) {
@@ -456,107 +460,111 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
   } else if (warp >= C::W_MMA) {
     regs_down<C::REG_MMA>();
     if (warp == C::W_Q && rank == 0) {
-      // ---- Q[tk] as nine TMA tiles (heads >= Hq arrive as zeros), tile i through ring i & 1 ----
-      RingPos<C::NLST> lp[2];
+      // ---- Q[tk] as nine TMA tiles (heads >= Hq arrive as zeros), two a stage use ----
       MlaSegIter segs = segs0;
       MlaSeg sg;
       bool ok = true;
-      RingPos<C::NLST> q_at[2];  // where the last token's Q tiles start and how many were issued
-      int q_issued = 0;
-      while (ok && segs.next(sg)) {
-        for (int i = 0; ok && i < MlaCfg::NSLAB_QK; ++i) {
-          RingPos<C::NLST>& at = (i & 1) ? lp[1] : lp[0];
-          const int slot = (i & 1) * C::NLST + at.slot;
-          if (!mbar_wait_warp(bars + C::B_RING_EMPTY + slot, at.ph ^ 1u, ab, 129)) { ok = false; break; }
-          if (i == 0) {  // the previous token's Q tiles have long been consumed
-            q_at[0] = lp[0];
-            q_at[1] = lp[1];
+      int n = 0, q_uses = 0;  // tokens, and stage uses of the last token's Q that were issued
+      for (; ok && segs.next(sg); ++n) {
+        const uint32_t par = static_cast<uint32_t>(n & 1);
+        for (int u = 0; u < C::Q_USES; ++u) {
+          const int st = u & 1;
+          if (!mbar_wait_warp(bars + C::B_RING_EMPTY + st, par ^ static_cast<uint32_t>((u >> 1) & 1) ^ 1u, ab, 129)) {
+            ok = false;
+            break;
           }
           if (lane == 0) {
-            uint64_t* full = bars + C::B_RING_FULL + slot;
-            mbar_arrive_expect_tx(full, C::SLAB_TILE);
-            tma_load_3d(smem + C::OFF_RING + slot * C::SLAB_TILE, &tmQ, full, i * 64, 0, sg.tk);
-            for (int a = 0; a < C::NPROD / 2; ++a) mbar_arrive(full);
+            uint64_t* full = bars + C::B_RING_FULL + st;
+            const int tiles = min(2, max(0, MlaCfg::NSLAB_QK - 2 * u));
+            if (tiles > 0) mbar_arrive_expect_tx(full, tiles * C::SLAB_TILE);
+            else mbar_arrive(full);
+            for (int i = 0; i < tiles; ++i)
+              tma_load_3d(smem + C::OFF_RING + st * C::STAGE + i * C::SLAB_TILE, &tmQ, full, (2 * u + i) * 64, 0,
+                          sg.tk);
+            for (int a = 0; a < C::NPROD; ++a) mbar_arrive(full);
           }
-          q_issued = i + 1;
+          q_uses = u + 1;  // (a free stage at u = 0 means that the previous token's Q has long been consumed)
           __syncwarp();
-          at.step(1);
         }
         // the uses that the producers fill
-        for (int i = 0; ok && i < (sg.c1 - sg.c0) * (C::NLAT / 2); ++i) {
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const int slot = g * C::NLST + lp[g].slot;
-            if (ok && !mbar_wait_warp(bars + C::B_RING_EMPTY + slot, lp[g].ph ^ 1u, ab, 124)) ok = false;
-            if (lane == 0 && ok) mbar_arrive(bars + C::B_RING_FULL + slot);
-            lp[g].step(1);
+        for (int k = 0; ok && k < 4 * (sg.c1 - sg.c0); ++k) {
+          if (!mbar_wait_warp(bars + C::B_RING_EMPTY + (k & 1), par ^ static_cast<uint32_t>((k >> 1) & 1), ab, 124)) {
+            ok = false;
+            break;
           }
+          if (lane == 0) mbar_arrive(bars + C::B_RING_FULL + (k & 1));
         }
       }
       if (lane == 0 && ab.raised()) {
-        // aborted: Q tiles may still be landing; wait for the latest use of each slot (bounded, whatever the flag says)
+        // aborted: Q tiles may still be landing; wait for the latest use of each stage (bounded, whatever the
+        // flag says). n counts the token as done unless its loop was left at Q.
         int never = 0;
         const AbortFlag no_abort{&never};
-        for (int i = 0; i < q_issued; ++i) {
-          RingPos<C::NLST>& w = (i & 1) ? q_at[1] : q_at[0];
-          if (i >= q_issued - 2 * C::NLST)
-            mbar_wait(bars + C::B_RING_FULL + (i & 1) * C::NLST + w.slot, w.ph, no_abort, 128);
-          w.step(1);
-        }
+        const uint32_t par = static_cast<uint32_t>((n - 1) & 1);
+        for (int u = max(0, q_uses - C::NST); u < q_uses; ++u)
+          mbar_wait(bars + C::B_RING_FULL + (u & 1), par ^ static_cast<uint32_t>((u >> 1) & 1), no_abort, 128);
       }
     } else if (warp == C::W_MMA && rank == 0) {
       // ---- score CTA's MMA warp: waits converged, one elected lane issues and commits ----
-      RingPos<C::NLST> lp[2];
       RingPos<C::NRST> rp;
       uint32_t sph = 1;
       uint32_t qfree_ph = 1;
       bool ok = true;
+      int n = 0;
       MlaSegIter segs = segs0;
       MlaSeg sg;
-      while (ok && segs.next(sg)) {
+      for (; ok && segs.next(sg); ++n) {
         // Q[tk] into TMEM once the previous piece's QK^T has read the old Q
         if (!mbar_wait_warp(bars + C::B_Q_FREE, qfree_ph, ab, 132)) break;
         qfree_ph ^= 1;
         tc_fence_after();
-        for (int i = 0; i < MlaCfg::NSLAB_QK; ++i) {
-          RingPos<C::NLST>& at = (i & 1) ? lp[1] : lp[0];
-          const int slot = (i & 1) * C::NLST + at.slot;
-          if (!mbar_wait_warp(bars + C::B_RING_FULL + slot, at.ph, ab, 140)) { ok = false; break; }
+        const uint32_t par = static_cast<uint32_t>(n & 1);
+#pragma unroll 1
+        for (int u = 0; u < C::Q_USES; ++u) {
+          const int st = u & 1;
+          if (!mbar_wait_warp(bars + C::B_RING_FULL + st, par ^ static_cast<uint32_t>((u >> 1) & 1), ab, 140)) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t tile = ring + slot * C::SLAB_TILE;
+            for (int i = 2 * u; i < min(2 * u + 2, MlaCfg::NSLAB_QK); ++i) {
+              const uint32_t tile = ring + st * C::STAGE + (i & 1) * C::SLAB_TILE;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_cp_128x256b(tmem + MlaCfg::Q_COL + (4 * i + kk) * 8, smem_desc(tile + kk * 32, 16, 1024, kSw128));
-            tc_commit(bars + C::B_RING_EMPTY + slot);
-            if (i == MlaCfg::NSLAB_QK - 1) tc_commit(bars + C::B_Q_IN);
+              for (int kk = 0; kk < 4; ++kk)
+                tc_cp_128x256b(tmem + MlaCfg::Q_COL + (4 * i + kk) * 8, smem_desc(tile + kk * 32, 16, 1024, kSw128));
+            }
+            tc_commit(bars + C::B_RING_EMPTY + st);
+            if (u == C::Q_USES - 1) tc_commit(bars + C::B_Q_IN);
           }
           __syncwarp();
-          at.step(1);
         }
         if (!ok) break;
+        const uint32_t d = tmem + MlaCfg::S_COL;
+#pragma unroll 1
         for (int j = sg.c0; j < sg.c1 && ok; ++j) {
           if (!mbar_wait_warp(bars + C::B_S_EMPTY, sph, ab, 134)) { ok = false; break; }
           sph ^= 1;
           tc_fence_after();
-          const uint32_t d = tmem + MlaCfg::S_COL;
-          for (int i = 0; i < C::NLAT; ++i) {
-            RingPos<C::NLST>& at = (i & 1) ? lp[1] : lp[0];
-            const int slot = (i & 1) * C::NLST + at.slot;
-            if (!mbar_wait_warp(bars + C::B_RING_FULL + slot, at.ph, ab, 133)) { ok = false; break; }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // slabs i and 4 + i
+            if (!mbar_wait_warp(bars + C::B_RING_FULL + (i & 1), par ^ 1u ^ static_cast<uint32_t>(i >> 1), ab, 133)) {
+              ok = false;
+              break;
+            }
             tc_fence_after();
             if (elect_one()) {
               fence_async_shared();
-              const uint32_t tile = ring + slot * C::SLAB_TILE;
-              const int slab = (i & 1) * 4 + (i >> 1);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_ts(d, tmem + MlaCfg::Q_COL + (4 * slab + kk) * 8, smem_desc(tile + kk * 32, 16, 1024, kSw128),
-                            MlaCfg::IDESC_QK, (i > 0 || kk > 0) ? 1u : 0u);
-              tc_commit(bars + C::B_RING_EMPTY + slot);
+              for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_bf16_ts(d, tmem + MlaCfg::Q_COL + (4 * (4 * t + i) + kk) * 8,
+                              smem_desc(ring + (i & 1) * C::STAGE + t * C::SLAB_TILE + kk * 32, 16, 1024, kSw128),
+                              MlaCfg::IDESC_QK, (i > 0 || t > 0 || kk > 0) ? 1u : 0u);
+              tc_commit(bars + C::B_RING_EMPTY + (i & 1));
             }
             __syncwarp();
-            at.step(1);
           }
           if (!ok) break;
           if (!mbar_wait_warp(bars + C::B_ROPE_FULL + rp.slot, rp.ph, ab, 135)) { ok = false; break; }
@@ -891,7 +899,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
   cluster_sync_all();
   if (warp == C::W_MMA) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(*tmem_base_s, 512);
   }
 }
 
