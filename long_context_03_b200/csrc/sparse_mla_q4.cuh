@@ -11,37 +11,43 @@
 // in TMEM, computes S = Q C^T for 128 rows at a time and the softmax, and
 // sends P to the value CTA, which accumulates O += P V in its whole TMEM. New
 // here is how the operand tiles come about:
-//   * Eight producer warps in each CTA copy codes and scales as they are
-//     (cp.async) into a queue in shared memory, one chunk ahead of their use,
-//     then expand them to bf16 and store them into the swizzled tiles that the
-//     MMA reads. One thread takes the 64 values of one row in one slab, for
-//     the copy as for the expansion, so its queue is its own and needs no
-//     barrier; its eight 16-byte stores fall into eight different bank groups
-//     for eight neighbouring rows. The loop is kept short on purpose: with the
-//     queue in registers it has to be unrolled over a chunk, and the code of
-//     all roles together then runs out of the instruction caches (measured: a
-//     quarter of all warp time waiting for instructions, 5.8 us a chunk).
-//   * The latent slabs of a chunk go through two stages of two tiles (slabs i
-//     and 4 + i, each filled by four of the warps): one wait, one proxy fence
-//     and one commit serve eight MMAs, whose 512 cycles cover what the issuing
-//     warp spends on them. With a wait for each tile it could not keep up (577
-//     cycles for 256 of MMA). The rotary slab (bf16 as it stands) is copied
-//     straight into two tiles of its own. Q's tiles pass through the stages
-//     too, in six uses (the sixth is empty), so that the uses of a stage and
-//     with them its parities are the same for every chunk of a token. A parity
-//     tells a phase only from its neighbours, so nobody may be two uses of a
-//     stage ahead or behind: the warp that loads Q also takes part in filling
-//     every other use (one arrival, after it has seen the stage free), and the
-//     producers pass over Q's uses only once a barrier of its own says that Q
-//     is in TMEM.
-//   * Page lookups and range checks are made once a token, when the index row
-//     is staged: the row numbers in shared memory are final (-1 for absent).
-//     Absent rows are copied as zero bytes, which stand for finite values,
-//     and get probability 0.
+//   * Four loader warps in each CTA read the selection, resolve pages, check
+//     ranges and copy the rows' codes and scales as they are (cp.async, 16
+//     lanes a row) into raw tiles in shared memory, about a chunk ahead of
+//     their use and across tokens. Absent rows are copied as zero bytes, which
+//     stand for finite values, and get probability 0. (Copies issued by the
+//     expanding warps, with their index and address arithmetic, cost those a
+//     third of their time; one bulk copy of 288 bytes a row takes the copy
+//     engine about 90 cycles a row, 105 us for 74 tokens.)
+//   * Eight warps expand the raw rows to bf16 and store them into the swizzled
+//     tiles that the MMA reads. A thread takes the 64 values of one row in one
+//     slab; its eight 16-byte stores fall into eight different bank groups for
+//     eight neighbouring rows, and so do its loads (raw rows are padded). The
+//     loop is kept short on purpose: unrolled over a chunk, with the codes in
+//     registers, the code of all roles together ran out of the instruction
+//     caches (a quarter of all warp time waiting for instructions, 5.8 us a
+//     chunk).
+//   * The latent slabs of a chunk go through two stages of two tiles (slabs
+//     2 i and 2 i + 1, each filled by four of the warps): one wait, one proxy
+//     fence and one commit serve eight MMAs, whose 512 cycles cover what the
+//     issuing warp spends on them. With a wait for each tile it could not keep
+//     up (577 cycles for 256 of MMA). The rotary slab (bf16 as it stands) is
+//     copied straight into a tile of its own and multiplied first, so that it has a chunk's time to arrive. Q's tiles pass through
+//     the stages too, in six uses (the sixth is empty), so that the uses of a
+//     stage and with them its parities are the same for every chunk of a
+//     token. A parity tells a phase only from its neighbours, so nobody may be
+//     two uses of a stage ahead or behind: the warp that loads Q also takes
+//     part in filling every other use (one arrival, after it has seen the
+//     stage free), and the expanding warps pass over Q's uses only once a
+//     barrier of its own says that Q is in TMEM.
 //   * The stores reach the tensor core's proxy by a fence on the MMA warp's
 //     side, between its wait for a tile and the first MMA on it.
-//   * Sixteen warps do not fit the softmax's registers at an even share, so
-//     the warp groups trade registers at the start.
+//   * Eight softmax warps, two a lane quarter with 64 columns each, exchange
+//     their rows' maxima through shared memory. Their code is straight-line
+//     and does not stay in the instruction caches, so a chunk takes as long as
+//     fetching it: four warps with 128 columns each took 4500 cycles.
+//   * The warp groups trade registers at the start (the softmax holds its
+//     scores).
 #pragma once
 
 #include "dsa_common.cuh"
@@ -57,46 +63,57 @@ struct MlaQ4Cfg {
   static constexpr int NST = 2;                        // latent stages of two tiles (score CTA)
   static constexpr int STAGE = 2 * SLAB_TILE;
   static constexpr int Q_USES = 6;                     // stage uses of a token's Q tiles
-  static constexpr int NRST = 2;                       // rotary tiles (score CTA)
   static constexpr int VROWS = MlaCfg::VROWS;
   static constexpr int VSLAB = MlaCfg::VSLAB;
   static constexpr int V_TILE = MlaCfg::V_TILE;
   static constexpr int NVST = 3;                       // value sub-tile ring (value CTA)
   static constexpr int NPB = MlaCfg::NPB;
-  static constexpr int NPROD = 8;                      // producer warps
-  static constexpr int W_SM0 = 8;                      // four softmax / epilogue warps
-  static constexpr int W_MMA = 12;
-  static constexpr int W_Q = 13;                       // loads Q's tiles (score CTA)
-  static constexpr int NTHREADS = 16 * 32;
-  // registers a thread after the trade: 2 * 96 + 208 + 80 <= 4 * 128
-  static constexpr int REG_PROD = 96, REG_SM = 208, REG_MMA = 80;
+  static constexpr int NPROD = 8;                      // expanding warps
+  static constexpr int W_SM0 = 8;                      // score: eight softmax warps; value: four epilogue warps
+  static constexpr int NSM = 8;
+  static constexpr int W_MMA = 16;
+  static constexpr int W_Q = 17;                       // loads Q's tiles (score CTA)
+  static constexpr int W_LOAD = 20;                    // loader warps
+  static constexpr int NLOAD = 4;
+  static constexpr int NTHREADS = 24 * 32;
+  // registers a thread at launch, and after the trade of the six warp groups
+  static constexpr int REG_LAUNCH = 65536 / NTHREADS / 8 * 8;
+  static constexpr int REG_PROD = 48, REG_SM = 128, REG_MMA = 64;
+  // Shared memory. The first part differs by CTA. Score: latent stages, the
+  // rotary tile, two raw chunks (rows of 288 bytes, padded to 304). Value:
+  // sub-tile ring, raw sub-tiles (32 rows), output staging.
   static constexpr int OFF_RING = 0;
-  static constexpr int OFF_ROPE = NST * STAGE;         // score CTA
-  static constexpr int RING_BYTES = NST * STAGE + NRST * SLAB_TILE;
-  static_assert(RING_BYTES == NVST * V_TILE, "the value ring takes the same space");
-  // The producers' queues: 4 entries of 32 bytes of codes a thread, in pieces
-  // of 16 bytes (piece i of thread t at (i * 256 + t) * 16). The scales: 4
-  // bytes an entry in the value CTA; 16 bytes a chunk, two chunks, in the
-  // score CTA, which has no use for the output staging.
-  static constexpr int NQ = 4;
-  static constexpr int OFF_FIFO = OFF_RING + RING_BYTES;
-  static constexpr int OFF_VSC = OFF_FIFO + NQ * 2 * NPROD * 32 * 16;
-  static constexpr int MSG_STRIDE = MlaCfg::MSG_STRIDE;
-  static constexpr int OFF_MSG = OFF_VSC + NQ * NPROD * 32 * 4;
-  static constexpr int OFF_IDX = OFF_MSG + NPB * MSG_STRIDE;
-  static constexpr int OFF_VMASK = OFF_IDX + MlaCfg::KMAX * 4;  // u32 [2][KMAX / 32]
-  static constexpr int OFF_EPI = (OFF_VMASK + 2 * (MlaCfg::KMAX / 32) * 4 + 1023) / 1024 * 1024;
+  static constexpr int OFF_ROPE = NST * STAGE;
+  static constexpr int RAW_ROW = kQ4Rope, RAW_PITCH = RAW_ROW + 16;
+  static constexpr int NRAW = 2, RAW_TILE = NK * RAW_PITCH;
+  static constexpr int OFF_RAW = OFF_ROPE + SLAB_TILE;
+  static constexpr int NVRAW = 4, VRAW_TILE = VROWS * RAW_PITCH;
+  static constexpr int OFF_VRAW = NVST * V_TILE;
+  static constexpr int OFF_EPI = OFF_VRAW + NVRAW * VRAW_TILE;
   static constexpr int EPI_TILE = MlaCfg::EPI_TILE;
-  static constexpr int OFF_SSC = OFF_EPI;
-  static_assert(2 * NPROD * 32 * 16 <= 4 * 2 * EPI_TILE, "the score CTA's scales");
-  static constexpr int OFF_BAR = OFF_EPI + 4 * 2 * EPI_TILE;
+  // A message to the value CTA: P, and the heads' rescale factors, a flag (any
+  // of them not 1), and after the last chunk the two partial row sums and the
+  // reference maximum of each head.
+  static constexpr int P_BYTES = MlaCfg::P_BYTES;
+  static constexpr int ST_ALPHA = 0, ST_CTRL = ST_ALPHA + MlaCfg::M * 4, ST_L = ST_CTRL + 16;
+  static constexpr int ST_M = ST_L + 2 * MlaCfg::M * 4, ST_STRIDE = ST_M + MlaCfg::M * 4;
+  static constexpr int ST_BYTES_MID = ST_L, ST_BYTES_LAST = ST_STRIDE;
+  static constexpr int OFF_MSG = (OFF_RAW + NRAW * RAW_TILE + 1023) / 1024 * 1024;
+  static_assert(OFF_EPI + 4 * 2 * EPI_TILE <= OFF_MSG && OFF_EPI % 128 == 0, "the value CTA's part");
+  static constexpr int OFF_STAT = OFF_MSG + NPB * P_BYTES;
+  static constexpr int OFF_XCH = OFF_STAT + NPB * ST_STRIDE;      // f32 [2][2][128]: the halves' row maxima
+  static constexpr int OFF_VMASK = OFF_XCH + 2 * 2 * MlaCfg::M * 4;  // u32 [4][4]: validity of four chunks' rows
+  static constexpr int OFF_BAR = OFF_VMASK + 64;
   // barriers (the same offsets in both CTAs)
   static constexpr int NRING = NST > NVST ? NST : NVST;   // score: [NST] stages; value: [NVST] sub-tiles
   static constexpr int B_RING_FULL = 0;
   static constexpr int B_RING_EMPTY = B_RING_FULL + NRING;
-  static constexpr int B_ROPE_FULL = B_RING_EMPTY + NRING;  // [NRST]
-  static constexpr int B_ROPE_EMPTY = B_ROPE_FULL + NRST;
-  static constexpr int B_S_FULL = B_ROPE_EMPTY + NRST;
+  static constexpr int B_RAW_FULL = B_RING_EMPTY + NRING;   // [NVRAW] (score: [NRAW])
+  static constexpr int B_RAW_EMPTY = B_RAW_FULL + NVRAW;
+  static_assert(NVRAW >= NRAW, "one set of barriers serves both CTAs");
+  static constexpr int B_ROPE_FULL = B_RAW_EMPTY + NVRAW;
+  static constexpr int B_ROPE_EMPTY = B_ROPE_FULL + 1;
+  static constexpr int B_S_FULL = B_ROPE_EMPTY + 1;
   static constexpr int B_S_EMPTY = B_S_FULL + 1;
   static constexpr int B_Q_FREE = B_S_EMPTY + 1;
   static constexpr int B_Q_IN = B_Q_FREE + 1;
@@ -105,15 +122,13 @@ struct MlaQ4Cfg {
   static constexpr int B_O_READY = B_P_FULL + NPB;         // [NPB]
   static constexpr int B_PV_DONE = B_O_READY + NPB;
   static constexpr int B_STAGE = B_PV_DONE + 1;
-  static constexpr int B_QUIESCE = B_STAGE + 1;
-  static constexpr int B_MASK_FULL = B_QUIESCE + 1;        // [2]
-  static constexpr int B_MASK_FREE = B_MASK_FULL + 2;      // [2]
-  static constexpr int B_PSTAGE = B_MASK_FREE + 2;
-  static constexpr int NBAR = B_PSTAGE + 1;
+  static constexpr int B_MAX = B_STAGE + 1;                // [4] row maxima of a lane quarter exchanged
+  static constexpr int B_QUIESCE = B_MAX + 4;
+  static constexpr int NBAR = B_QUIESCE + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 32;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-  static_assert(2 * REG_PROD + REG_SM + REG_MMA <= 4 * (65536 / NTHREADS), "register trade");
+  static_assert(2 * REG_PROD + 2 * REG_SM + 2 * REG_MMA <= NTHREADS / 128 * REG_LAUNCH, "register trade");
 };
 
 // The base parameters' kv and kv_token_stride are unused; rows, paging and
@@ -164,32 +179,30 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void cp_async_4_zfill(uint32_t dst, const void* src, bool valid) {
-  const uint32_t n = valid ? 4u : 0u;
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+// The 64 values of a row in one slab: 8 words of codes, 4 scale bytes.
+struct RowCodes {
+  uint4 lo, hi;
+  uint32_t scales;
+};
+__device__ __forceinline__ RowCodes load_row(uint32_t codes, uint32_t scales) {
+  RowCodes c;
+  c.lo = lds128(codes);
+  c.hi = lds128(codes + 16);
+  c.scales = lds32(scales);
+  return c;
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
-
-// 64 values of a row (two 16-byte pieces of codes `step` bytes apart, 4 scale
-// bytes) into its 128 bytes of a swizzled tile: piece c goes to c ^ (row & 7).
-__device__ __forceinline__ void expand_row(uint32_t row_addr, uint32_t swz, uint32_t codes, uint32_t step,
-                                           uint32_t scales) {
+// Expanded to their 128 bytes of a swizzled tile: piece i goes to i ^ (row & 7).
+__device__ __forceinline__ void expand_row(uint32_t row_addr, uint32_t swz, const RowCodes& c) {
+  const uint32_t w[8] = {c.lo.x, c.lo.y, c.lo.z, c.lo.w, c.hi.x, c.hi.y, c.hi.z, c.hi.w};
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint4 w4 = lds128(codes + h * step);
-    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t s2 = q4_scale_pair((scales >> (8 * (2 * h + (i >> 1)))) & 0xffu);
-      const uint32_t off2 = q4_offset_pair(s2);
-      uint32_t v[4];
-      q4_values(w[i], s2, off2, v);
-      sts128(row_addr + (static_cast<uint32_t>((4 * h + i) << 4) ^ swz), v);
-    }
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t s2 = q4_scale_pair((c.scales >> (8 * g)) & 0xffu);
+    const uint32_t off2 = q4_offset_pair(s2);
+    uint32_t v[2][4];
+    q4_values(w[2 * g], s2, off2, v[0]);
+    q4_values(w[2 * g + 1], s2, off2, v[1]);
+    sts128(row_addr + (static_cast<uint32_t>((2 * g) << 4) ^ swz), v[0]);
+    sts128(row_addr + (static_cast<uint32_t>((2 * g + 1) << 4) ^ swz), v[1]);
   }
 }
 
@@ -212,46 +225,25 @@ __device__ __forceinline__ void token_rows_q4(const MlaQ4Params& p, int tk, long
   }
 }
 
-// The producer warps put a token's selection into shared memory as row
-// numbers from the token's first row (of the pool when paged), -1 where there
-// is none: past topk, negative, outside the cache or behind a page outside
-// the pool (both reported). Its threads meet twice on the mbarrier `stage`
-// (the previous row is no longer read; the new one is written), with bounded
-// waits. Writes the validity bits of each 32 entries when vmask is given.
+// Entry e of token tk's selection as a row number from the token's first row
+// (of the pool when paged), or -1: past topk, negative, outside the cache or
+// behind a page outside the pool (the last two reported).
 template <bool kPaged>
-__device__ __forceinline__ bool stage_rows_q4(int32_t* idx_s, uint32_t* vmask, const MlaQ4Params& p, int tk, int nent,
-                                              int rows, int ptid, uint64_t* stage, uint32_t& phase, AbortFlag ab) {
-  mbar_arrive(stage);
-  if (!mbar_wait(stage, phase, ab, 126)) return false;
-  phase ^= 1u;
-  const int32_t* src = p.idx + static_cast<size_t>(tk) * p.K;
-  for (int e = ptid; e < nent; e += MlaQ4Cfg::NPROD * 32) {  // nent is a multiple of 32: whole warps
-    int row = e < p.K ? __ldg(src + e) : -1;
-    bool bad = row >= rows;
-    if constexpr (kPaged) {
-      if (row >= 0 && !bad) {
-        const int page = __ldg(p.block_table + static_cast<long long>(tk) * p.bt_stride + (row >> p.page_shift));
-        const long long phys =
-            (static_cast<long long>(page) << p.page_shift) + (row & ((1 << p.page_shift) - 1));
-        bad = page < 0 || phys >= p.pool_rows;
-        row = static_cast<int>(phys);
-      }
-    }
-    if (bad) {
-      set_device_error(kErrBadIndex, 4);
-      row = -1;
-    }
-    row = max(row, -1);
-    idx_s[e] = row;
-    if (vmask) {
-      const uint32_t m = __ballot_sync(0xffffffffu, row >= 0);
-      if ((e & 31) == 0) vmask[e >> 5] = m;
+__device__ __forceinline__ int resolve_row_q4(const MlaQ4Params& p, int tk, int row, int rows) {
+  bool bad = row >= rows;
+  if constexpr (kPaged) {
+    if (row >= 0 && !bad) {
+      const int page = __ldg(p.block_table + static_cast<long long>(tk) * p.bt_stride + (row >> p.page_shift));
+      const long long phys = (static_cast<long long>(page) << p.page_shift) + (row & ((1 << p.page_shift) - 1));
+      bad = page < 0 || phys >= p.pool_rows;
+      row = static_cast<int>(phys);
     }
   }
-  mbar_arrive(stage);
-  if (!mbar_wait(stage, phase, ab, 127)) return false;
-  phase ^= 1u;
-  return true;
+  if (bad) {
+    set_device_error(kErrBadIndex, 4);
+    return -1;
+  }
+  return max(row, -1);
 }
 
 template <bool kPaged>
@@ -264,7 +256,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
   uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   int* abort_s = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
   int* rescale_s = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);
-  int32_t* idx_s = reinterpret_cast<int32_t*>(smem + C::OFF_IDX);
   uint32_t* vmask_s = reinterpret_cast<uint32_t*>(smem + C::OFF_VMASK);
   const AbortFlag ab{abort_s};
   const uint32_t rank = cluster_ctarank();
@@ -284,12 +275,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
       mbar_init(bars + C::B_RING_FULL + i, rank == 0 ? C::NPROD + 1 : C::NPROD);  // the producer warps, and Q's
       mbar_init(bars + C::B_RING_EMPTY + i, 1);
     }
-    for (int i = 0; i < C::NRST; ++i) {
-      mbar_init(bars + C::B_ROPE_FULL + i, C::NPROD * 32);
-      mbar_init(bars + C::B_ROPE_EMPTY + i, 1);
+    for (int i = 0; i < C::NVRAW; ++i) {
+      mbar_init(bars + C::B_RAW_FULL + i, C::NLOAD * 33);  // the loaders' lanes, and a plain arrival each
+      mbar_init(bars + C::B_RAW_EMPTY + i, C::NPROD);
     }
-    mbar_init(bars + C::B_S_FULL, 1);
-    mbar_init(bars + C::B_S_EMPTY, 4);
+    mbar_init(bars + C::B_ROPE_FULL, C::NLOAD * 32);
+    mbar_init(bars + C::B_ROPE_EMPTY, 1);
+    mbar_init(bars + C::B_S_FULL, 2);  // the MMAs' completion, and their issuer (it carries the masks' visibility)
+    mbar_init(bars + C::B_S_EMPTY, C::NSM);
     mbar_init(bars + C::B_Q_FREE, 1);
     mbar_init(bars + C::B_Q_IN, 1);
     for (int i = 0; i < C::NPB; ++i) {
@@ -298,13 +291,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
       mbar_init(bars + C::B_O_READY + i, 4);
     }
     mbar_init(bars + C::B_PV_DONE, 1);
-    mbar_init(bars + C::B_STAGE, 4);
+    mbar_init(bars + C::B_STAGE, C::NSM);
+    for (int i = 0; i < 4; ++i) mbar_init(bars + C::B_MAX + i, 2);
     mbar_init(bars + C::B_QUIESCE, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bars + C::B_MASK_FULL + i, C::NPROD);
-      mbar_init(bars + C::B_MASK_FREE + i, 4);
-    }
-    mbar_init(bars + C::B_PSTAGE, C::NPROD * 32);
     fence_mbar_init();
   }
   if (warp == C::W_MMA) tmem_alloc(tmem_base_s, 512);
@@ -314,7 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
   if (rank == 1 && threadIdx.x == 0) {
     for (int i = 0; i < C::NPB && i < total_msgs; ++i) {
       const bool last = segs0.last_of_piece(i);
-      mbar_arrive_expect_tx(bars + C::B_P_FULL + i, last ? MlaCfg::MSG_BYTES_LAST : MlaCfg::MSG_BYTES_MID);
+      mbar_arrive_expect_tx(bars + C::B_P_FULL + i, C::P_BYTES + (last ? C::ST_BYTES_LAST : C::ST_BYTES_MID));
     }
   }
   cluster_sync_all();
@@ -322,144 +311,157 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
   tc_fence_after();
   constexpr uint32_t tmem = 0;  // the CTA holds all 512 columns, so they start at 0
   const uint32_t ring = smem_u32(smem + C::OFF_RING);
-  const uint32_t rope_ring = smem_u32(smem + C::OFF_ROPE);
+  const uint32_t rope_tile = smem_u32(smem + C::OFF_ROPE);
   const uint32_t msg = smem_u32(smem + C::OFF_MSG);
 
   if (warp < C::NPROD) {
     regs_down<C::REG_PROD>();
     const int ptid = threadIdx.x;
-    uint32_t stage_ph = 0;
     MlaSegIter segs = segs0;
     MlaSeg sg;
+    bool ok = true;
     if (rank == 0) {
-      // ---- score CTA: latent tiles (row r of the chunk, slabs 4 grp ..) and rotary tiles ----
+      // ---- score CTA: row r of the chunk, in stage use i slab 2 i + grp ----
       const int grp = ptid >> 7;
       const int r = ptid & 127;
       const uint32_t swz = static_cast<uint32_t>(r & 7) << 4;
-      const int rc = ptid & 7, rr = ptid >> 3;  // rotary: piece rc of rows rr + 32 k
       const uint32_t ltile = ring + grp * C::SLAB_TILE + r * 128;
-      RingPos<C::NRST> rp;
-      constexpr uint32_t kQueue = C::NPROD * 32 * 16;
-      const uint32_t codes_q = smem_u32(smem + C::OFF_FIFO) + ptid * 16, sc_q = smem_u32(smem + C::OFF_SSC) + ptid * 16;
-      int n = 0;
-      bool ok = true;
-      for (; ok && segs.next(sg); ++n) {
-        long long first;
-        int trows;
-        token_rows_q4(p, sg.tk, first, trows);
-        const uint8_t* base = p.cache + first * kQ4RowBytes;
-        const int mb = n & 1;
-        if (!mbar_wait(bars + C::B_MASK_FREE + mb, ((n >> 1) & 1) ^ 1, ab, 130)) break;
-        if (!stage_rows_q4<kPaged>(idx_s, vmask_s + mb * (MlaCfg::KMAX / 32), p, sg.tk, nchunk * C::NK, trows, ptid,
-                                   bars + C::B_PSTAGE, stage_ph, ab))
-          break;
-        if (lane == 0) mbar_arrive(bars + C::B_MASK_FULL + mb);
-        // copies of chunk j: this thread's row (codes of one slab an entry,
-        // the group's 16 scale bytes with the first) and its rotary pieces
-        const uint8_t* row = nullptr;
-        auto copy_codes = [&](int j, int i) {
-          if (i == 0) {
-            const int rn = idx_s[j * C::NK + r];
-            row = rn >= 0 ? base + static_cast<long long>(rn) * kQ4RowBytes : nullptr;
-            cp_async_16_zfill(sc_q + (j & 1) * kQueue, (row ? row : p.cache) + kQ4Scales + 16 * grp, row != nullptr);
-          }
-          const uint8_t* src = (row ? row : p.cache) + (4 * grp + i) * 32;
-          cp_async_16_zfill(codes_q + (2 * i) * kQueue, src, row != nullptr);
-          cp_async_16_zfill(codes_q + (2 * i + 1) * kQueue, src + 16, row != nullptr);
-        };
-        auto copy_rope = [&](int j) {
-          const uint32_t rt = rope_ring + rp.slot * C::SLAB_TILE + rr * 128 + ((rc ^ (rr & 7)) << 4);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int rn = idx_s[j * C::NK + rr + 32 * k];
-            const uint8_t* src = rn >= 0 ? base + static_cast<long long>(rn) * kQ4RowBytes : p.cache;
-            cp_async_16_zfill(rt + k * 32 * 128, src + kQ4Rope + 16 * rc, rn >= 0);
-          }
-          cp_async_mbar_arrive(bars + C::B_ROPE_FULL + rp.slot);
-          rp.step(1);
-        };
-        // the first chunk's copies, one group an entry
-        if (!mbar_wait(bars + C::B_ROPE_EMPTY + rp.slot, rp.ph ^ 1u, ab, 132)) break;
-        copy_rope(sg.c0);
-#pragma unroll 1
-        for (int i = 0; i < C::NQ; ++i) {
-          copy_codes(sg.c0, i);
-          cp_async_commit();
-        }
+      const uint32_t raw = smem_u32(smem + C::OFF_RAW) + r * C::RAW_PITCH;
+      RingPos<C::NRAW> rd;
+      for (int n = 0; ok && segs.next(sg); ++n) {
         if (!mbar_wait(bars + C::B_Q_IN, n & 1, ab, 125)) break;  // Q's tiles go first
         // parity of a stage's first use in a chunk: three uses a token by Q, two a chunk
         const uint32_t par = static_cast<uint32_t>(n & 1) ^ 1u;
+        for (int j = sg.c0; ok && j < sg.c1; ++j) {
+          if (!mbar_wait(bars + C::B_RAW_FULL + rd.slot, rd.ph, ab, 122)) { ok = false; break; }
+          const uint32_t row = raw + rd.slot * C::RAW_TILE;
 #pragma unroll 1
-        for (int k = 4 * sg.c0; k < 4 * sg.c1; ++k) {
-          const int j = k >> 2, i = k & 3;
-          cp_async_wait<C::NQ - 1>();  // this entry has landed
-          if (!mbar_wait(bars + C::B_RING_EMPTY + (i & 1), par ^ static_cast<uint32_t>(i >> 1) ^ 1u, ab, 131)) {
-            ok = false;
-            break;
-          }
-          expand_row(ltile + (i & 1) * C::STAGE, swz, codes_q + 2 * i * kQueue, kQueue,
-                     lds32(sc_q + (j & 1) * kQueue + 4 * i));
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bars + C::B_RING_FULL + (i & 1));
-          if (j + 1 < sg.c1) {
-            copy_codes(j + 1, i);
-            if (i == 3) {
-              // the slot's last use was two chunks back: over, since this chunk's first tiles have been read
-              if (!mbar_wait(bars + C::B_ROPE_EMPTY + rp.slot, rp.ph ^ 1u, ab, 132)) { ok = false; break; }
-              copy_rope(j + 1);
+          for (int i = 0; i < 4; ++i) {
+            const int st = i & 1, slab = 2 * i + grp;
+            const RowCodes rc = load_row(row + slab * 32, row + kQ4Scales + slab * 4);
+            if (!mbar_wait(bars + C::B_RING_EMPTY + st, par ^ static_cast<uint32_t>(i >> 1) ^ 1u, ab, 131)) {
+              ok = false;
+              break;
             }
+            expand_row(ltile + st * C::STAGE, swz, rc);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + C::B_RING_FULL + st);
           }
-          cp_async_commit();
+          if (lane == 0) mbar_arrive(bars + C::B_RAW_EMPTY + rd.slot);
+          rd.step(1);
         }
       }
     } else {
       // ---- value CTA: 32-row sub-tiles; warp = slab, lane = row ----
       const uint32_t swz = (lane & 7u) << 4;
-      const uint32_t row_off = warp * C::VSLAB + lane * 128;
+      const uint32_t vtile = ring + warp * C::VSLAB + lane * 128;
+      const uint32_t raw = smem_u32(smem + C::OFF_VRAW) + lane * C::RAW_PITCH;
       RingPos<C::NVST> vp;
-      constexpr uint32_t kQueue = C::NPROD * 32 * 16;
-      const uint32_t codes_q = smem_u32(smem + C::OFF_FIFO) + ptid * 16, sc_q = smem_u32(smem + C::OFF_VSC) + ptid * 4;
+      RingPos<C::NVRAW> rd;
+      const int total = total_msgs * (C::NK / C::VROWS);
+#pragma unroll 1
+      for (int k = 0; k < total; ++k) {
+        if (!mbar_wait(bars + C::B_RAW_FULL + rd.slot, rd.ph, ab, 122)) break;
+        const uint32_t row = raw + rd.slot * C::VRAW_TILE;
+        const RowCodes rc = load_row(row + warp * 32, row + kQ4Scales + warp * 4);
+        if (!mbar_wait(bars + C::B_RING_EMPTY + vp.slot, vp.ph ^ 1u, ab, 141)) break;
+        expand_row(vtile + vp.slot * C::V_TILE, swz, rc);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bars + C::B_RING_FULL + vp.slot);
+          mbar_arrive(bars + C::B_RAW_EMPTY + rd.slot);
+        }
+        vp.step(1);
+        rd.step(1);
+      }
+    }
+  } else if (warp >= C::W_MMA) {
+    regs_down<C::REG_MMA>();
+    if (warp >= C::W_LOAD) {
+      // ---- loaders: each a quarter of a tile's rows (score: 32 of 128, with their rotary values; value: 8 of 32) ----
+      const int part = static_cast<int>(warp) - C::W_LOAD;
+      const int tile_rows = rank == 0 ? C::NK : C::VROWS;
+      const uint32_t nraw = rank == 0 ? C::NRAW : C::NVRAW;
+      const uint32_t raw = smem_u32(smem + (rank == 0 ? C::OFF_RAW : C::OFF_VRAW));
+      const uint32_t tile_bytes = rank == 0 ? C::RAW_TILE : C::VRAW_TILE;
+      const int my_rows = tile_rows / C::NLOAD, row0 = part * my_rows;  // 32 or 8
+      const int ln = static_cast<int>(lane);
+      uint32_t use = 0;  // raw tiles filled
+      uint32_t rope_ph = 1;
       bool ok = true;
+      MlaSegIter segs = segs0;
+      MlaSeg sg;
       while (ok && segs.next(sg)) {
         long long first;
         int trows;
         token_rows_q4(p, sg.tk, first, trows);
         const uint8_t* base = p.cache + first * kQ4RowBytes;
-        if (!stage_rows_q4<kPaged>(idx_s, nullptr, p, sg.tk, nchunk * C::NK, trows, ptid, bars + C::B_PSTAGE,
-                                   stage_ph, ab))
-          break;
-        auto copy_sub = [&](int k) {  // entry k: rows 32 k .. of the selection
-          const int rn = idx_s[k * C::VROWS + static_cast<int>(lane)];
-          const uint8_t* row = rn >= 0 ? base + static_cast<long long>(rn) * kQ4RowBytes : p.cache;
-          const int i = k & 3;
-          cp_async_16_zfill(codes_q + (2 * i) * kQueue, row + warp * 32, rn >= 0);
-          cp_async_16_zfill(codes_q + (2 * i + 1) * kQueue, row + warp * 32 + 16, rn >= 0);
-          cp_async_4_zfill(sc_q + i * (kQueue / 4), row + kQ4Scales + 4 * warp, rn >= 0);
+        const int32_t* sel = p.idx + static_cast<size_t>(sg.tk) * p.K;
+        const int e1 = sg.c1 * C::NK;
+        auto fetch = [&](int e) {  // entry of row `lane` of this warp's part of the tile at e
+          const int k = e + row0 + ln;
+          return (ln < my_rows && k < min(e1, p.K)) ? __ldg(sel + k) : -1;
         };
+        int nxt = fetch(sg.c0 * C::NK);
 #pragma unroll 1
-        for (int i = 0; i < C::NQ; ++i) {
-          copy_sub(4 * sg.c0 + i);
-          cp_async_commit();
-        }
+        for (int e0 = sg.c0 * C::NK; e0 < e1; e0 += tile_rows, ++use) {
+          const int row = resolve_row_q4<kPaged>(p, sg.tk, nxt, trows);
+          nxt = fetch(e0 + tile_rows);
+          // kCount 16-byte pieces: piece u goes to dst(u) from `off` bytes into the cache row of lane of(u). The
+          // exchanges come first and the copies after them, so that their latencies overlap.
+          auto copy_pieces = [&](auto count, auto of, auto dst, int off) {
+            constexpr int kCount = decltype(count)::value;
+            int rn[kCount];
+#pragma unroll
+            for (int u = 0; u < kCount; ++u) rn[u] = __shfl_sync(0xffffffffu, row, of(u));
+#pragma unroll
+            for (int u = 0; u < kCount; ++u)
+              cp_async_16_zfill(dst(u), (rn[u] >= 0 ? base + static_cast<long long>(rn[u]) * kQ4RowBytes : p.cache) + off,
+                                rn[u] >= 0);
+          };
+          using Four = std::integral_constant<int, 4>;
+          using One = std::integral_constant<int, 1>;
+          const uint32_t slot = use % nraw;
+          uint64_t* full = bars + C::B_RAW_FULL + slot;
+          if (!mbar_wait_warp(bars + C::B_RAW_EMPTY + slot, ((use / nraw) & 1u) ^ 1u, ab, 123)) { ok = false; break; }
+          const uint32_t tile = raw + slot * tile_bytes + row0 * C::RAW_PITCH;
+          if (rank == 0) {
+            // (the entry of four chunks ago has been read: its chunk's scores were read before this tile was free)
+            const uint32_t m = __ballot_sync(0xffffffffu, row >= 0);
+            if (lane == 0) vmask_s[(use & 3u) * 4 + part] = m;
+          }
 #pragma unroll 1
-        for (int k = 4 * sg.c0; k < 4 * sg.c1; ++k) {
-          const int i = k & 3;
-          cp_async_wait<C::NQ - 1>();
-          if (!mbar_wait(bars + C::B_RING_EMPTY + vp.slot, vp.ph ^ 1u, ab, 141)) { ok = false; break; }
-          expand_row(ring + vp.slot * C::V_TILE + row_off, swz, codes_q + 2 * i * kQueue, kQueue,
-                     lds32(sc_q + i * (kQueue / 4)));
+          for (int m = 0; m < my_rows; m += 8)
+            copy_pieces(Four{}, [&](int u) { return m + 2 * u + (ln >> 4); },
+                        [&](int u) { return tile + (m + 2 * u + (ln >> 4)) * C::RAW_PITCH + (ln & 15) * 16; },
+                        (ln & 15) * 16);
+#pragma unroll 1
+          for (int m = 0; m < my_rows; m += 16)
+            {
+              // (with 8 rows the upper lanes repeat the lower ones' copies)
+              const int r = (m + (ln >> 1)) & (my_rows - 1);
+              copy_pieces(One{}, [&](int) { return r; },
+                          [&](int) { return tile + r * C::RAW_PITCH + kQ4Scales + (ln & 1) * 16; },
+                          kQ4Scales + (ln & 1) * 16);
+            }
+          cp_async_mbar_arrive(full);
           __syncwarp();
-          if (lane == 0) mbar_arrive(bars + C::B_RING_FULL + vp.slot);
-          if (k + C::NQ < 4 * sg.c1) copy_sub(k + C::NQ);
-          cp_async_commit();
-          vp.step(1);
+          if (lane == 0) mbar_arrive(full);  // (makes the masks visible)
+          if (rank == 0) {
+            if (!mbar_wait_warp(bars + C::B_ROPE_EMPTY, rope_ph, ab, 132)) { ok = false; break; }
+            rope_ph ^= 1u;
+            const uint32_t rope = rope_tile + (row0 + (ln >> 3)) * 128 + (((ln & 7) ^ (ln >> 3)) << 4);
+#pragma unroll 1
+            for (int m = 0; m < 32; m += 16)
+              copy_pieces(Four{}, [&](int u) { return m + 4 * u + (ln >> 3); },
+                          [&](int u) { return (rope + (m + 4 * u) * 128) ^ ((u & 1) << 6); },
+                          kQ4Rope + (ln & 7) * 16);
+            cp_async_mbar_arrive(bars + C::B_ROPE_FULL);
+          }
         }
       }
-    }
-    cp_async_wait<0>();
-  } else if (warp >= C::W_MMA) {
-    regs_down<C::REG_MMA>();
-    if (warp == C::W_Q && rank == 0) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == C::W_Q && rank == 0) {
       // ---- Q[tk] as nine TMA tiles (heads >= Hq arrive as zeros), two a stage use ----
       MlaSegIter segs = segs0;
       MlaSeg sg;
@@ -506,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
       }
     } else if (warp == C::W_MMA && rank == 0) {
       // ---- score CTA's MMA warp: waits converged, one elected lane issues and commits ----
-      RingPos<C::NRST> rp;
+      uint32_t rope_ph = 0;
       uint32_t sph = 1;
       uint32_t qfree_ph = 1;
       bool ok = true;
@@ -545,9 +547,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
         for (int j = sg.c0; j < sg.c1 && ok; ++j) {
           if (!mbar_wait_warp(bars + C::B_S_EMPTY, sph, ab, 134)) { ok = false; break; }
           sph ^= 1;
+          if (!mbar_wait_warp(bars + C::B_ROPE_FULL, rope_ph, ab, 135)) { ok = false; break; }
+          rope_ph ^= 1;
           tc_fence_after();
+          if (elect_one()) {
+            fence_async_shared();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // slabs i and 4 + i
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_ts(d, tmem + MlaCfg::Q_COL + (4 * C::NLAT + kk) * 8,
+                          smem_desc(rope_tile + kk * 32, 16, 1024, kSw128), MlaCfg::IDESC_QK, kk > 0 ? 1u : 0u);
+            tc_commit(bars + C::B_ROPE_EMPTY);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // slabs 2 i and 2 i + 1
             if (!mbar_wait_warp(bars + C::B_RING_FULL + (i & 1), par ^ 1u ^ static_cast<uint32_t>(i >> 1), ab, 133)) {
               ok = false;
               break;
@@ -559,29 +572,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
               for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                  mma_bf16_ts(d, tmem + MlaCfg::Q_COL + (4 * (4 * t + i) + kk) * 8,
+                  mma_bf16_ts(d, tmem + MlaCfg::Q_COL + (4 * (2 * i + t) + kk) * 8,
                               smem_desc(ring + (i & 1) * C::STAGE + t * C::SLAB_TILE + kk * 32, 16, 1024, kSw128),
-                              MlaCfg::IDESC_QK, (i > 0 || t > 0 || kk > 0) ? 1u : 0u);
+                              MlaCfg::IDESC_QK, 1u);
               tc_commit(bars + C::B_RING_EMPTY + (i & 1));
+              if (i == 3) {
+                mbar_arrive(bars + C::B_S_FULL);
+                tc_commit(bars + C::B_S_FULL);
+                if (j == sg.c1 - 1) tc_commit(bars + C::B_Q_FREE);
+              }
             }
             __syncwarp();
           }
-          if (!ok) break;
-          if (!mbar_wait_warp(bars + C::B_ROPE_FULL + rp.slot, rp.ph, ab, 135)) { ok = false; break; }
-          tc_fence_after();
-          if (elect_one()) {
-            fence_async_shared();
-            const uint32_t tile = rope_ring + rp.slot * C::SLAB_TILE;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16_ts(d, tmem + MlaCfg::Q_COL + (4 * C::NLAT + kk) * 8, smem_desc(tile + kk * 32, 16, 1024, kSw128),
-                          MlaCfg::IDESC_QK, 1u);
-            tc_commit(bars + C::B_ROPE_EMPTY + rp.slot);
-            tc_commit(bars + C::B_S_FULL);
-            if (j == sg.c1 - 1) tc_commit(bars + C::B_Q_FREE);
-          }
-          __syncwarp();
-          rp.step(1);
         }
       }
     } else if (warp == C::W_MMA) {
@@ -597,7 +599,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
         for (int j = sg.c0; j < sg.c1 && ok; ++j) {
           if (!mbar_wait_warp(bars + C::B_P_FULL + pb, pph, ab, 143)) { ok = false; break; }
           const uint32_t any_rs =
-              reinterpret_cast<const volatile uint32_t*>(smem + C::OFF_MSG + pb * C::MSG_STRIDE + MlaCfg::MSG_CTRL)[0];
+              reinterpret_cast<const volatile uint32_t*>(smem + C::OFF_STAT + pb * C::ST_STRIDE + C::ST_CTRL)[0];
           // A rescale needs O quiescent: commit everything issued so far to
           // QUIESCE; the correction warps wait on it, rescale, then signal O_READY.
           if (any_rs && j > sg.c0) {
@@ -606,7 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
           }
           if (!mbar_wait_warp(bars + C::B_O_READY + pb, pph, ab, 144)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t pbase = msg + pb * C::MSG_STRIDE;
+          const uint32_t pbase = msg + pb * C::P_BYTES;
           for (int u = 0; u < C::NK / C::VROWS; ++u) {
             if (!mbar_wait_warp(bars + C::B_RING_FULL + vp.slot, vp.ph, ab, 142)) { ok = false; break; }
             tc_fence_after();
@@ -631,7 +633,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
                 if (nxt < total_msgs) {
                   const bool lastm = segs0.last_of_piece(nxt);
                   mbar_arrive_expect_tx(bars + C::B_P_FULL + pb,
-                                        lastm ? MlaCfg::MSG_BYTES_LAST : MlaCfg::MSG_BYTES_MID);
+                                        C::P_BYTES + (lastm ? C::ST_BYTES_LAST : C::ST_BYTES_MID));
                 }
               }
             }
@@ -650,20 +652,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
     const int h = quarter * 32 + static_cast<int>(lane);  // thread = head row (TMEM lane)
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     if (rank == 0) {
-      // ---- softmax ----
+      // ---- softmax: thread = head row and half of the chunk's 128 columns ----
+      const int half = static_cast<int>(warp - C::W_SM0) >> 2;
       const uint32_t peer_msg = map_to_peer(msg, 1);
+      const uint32_t peer_stat = map_to_peer(smem_u32(smem + C::OFF_STAT), 1);
       const uint32_t peer_pfull = map_to_peer(smem_u32(bars + C::B_P_FULL), 1);
+      float* xch = reinterpret_cast<float*>(smem + C::OFF_XCH);
       uint32_t sph = 0;
       int pb = 0;
       uint32_t pfree_ph = 1;
-      uint32_t stage_ph = 0;
       bool ok = true;
-      int n = 0;
+      int chunk = 0;  // chunks done by this cluster
       MlaSegIter segs = segs0;
       MlaSeg sg;
-      for (; ok && segs.next(sg); ++n) {
+      while (ok && segs.next(sg)) {
         const int ntk = segs.next_token();
-        if (h == 0 && ntk >= 0 && ntk != sg.tk) {
+        if (h == 0 && half == 0 && ntk >= 0 && ntk != sg.tk) {
           // warm L2 with the next piece's queries
           const char* nq = reinterpret_cast<const char*>(p.q + static_cast<size_t>(ntk) * p.Hq * MlaCfg::D);
           const uint32_t qbytes = static_cast<uint32_t>(p.Hq) * MlaCfg::D * 2;
@@ -671,31 +675,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
         }
         float m_ref = -INFINITY;
         float l_sum = 0.f;
-        const int mb = n & 1;
-        if (!mbar_wait(bars + C::B_MASK_FULL + mb, (n >> 1) & 1, ab, 139)) break;
-        const uint4* vm_tok = reinterpret_cast<const uint4*>(vmask_s + mb * (MlaCfg::KMAX / 32));
-        for (int j = sg.c0; j < sg.c1; ++j) {
-          const uint4 vm4 = vm_tok[j];
-          const uint32_t vmask[4] = {vm4.x, vm4.y, vm4.z, vm4.w};
+        for (int j = sg.c0; j < sg.c1; ++j, ++chunk) {
           if (!mbar_wait(bars + C::B_S_FULL, sph, ab, 136)) { ok = false; break; }
           sph ^= 1;
           tc_fence_after();
-          // this head's 128 scores into registers; the S buffer goes back to
-          // the tensor core at once
-          const uint32_t s_addr = tmem + lane_addr + MlaCfg::S_COL;
-          uint32_t sr[4][32];
+          const uint2 vm2 = reinterpret_cast<const uint2*>(vmask_s)[(chunk & 3) * 2 + half];  // validity of the rows
+          const uint32_t vmask[2] = {vm2.x, vm2.y};
+          // this thread's 64 scores into registers; the S buffer goes back to the tensor core at once
+          const uint32_t s_addr = tmem + lane_addr + MlaCfg::S_COL + half * 64;
+          uint32_t sr[2][32];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) tmem_ld32_nowait(s_addr + g * 32, sr[g]);
+          for (int g = 0; g < 2; ++g) tmem_ld32_nowait(s_addr + g * 32, sr[g]);
 #pragma unroll
-          for (int g = 0; g < 4; ++g) tmem_ld_wait_fence(sr[g]);
+          for (int g = 0; g < 2; ++g) tmem_ld_wait_fence(sr[g]);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bars + C::B_S_EMPTY);
           // absent rows score -inf (a chunk without any is the common case)
-          const bool all_valid = (vmask[0] & vmask[1] & vmask[2] & vmask[3]) == 0xffffffffu;
-          if (!all_valid) {
+          if ((vmask[0] & vmask[1]) != 0xffffffffu) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
+            for (int g = 0; g < 2; ++g)
 #pragma unroll
               for (int c = 0; c < 32; ++c)
                 if (!((vmask[g] >> c) & 1u)) sr[g][c] = 0xff800000u;
@@ -703,11 +702,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
           float mx[4];
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            mx[g] = __uint_as_float(sr[g][0]);
+            mx[g] = __uint_as_float(sr[g >> 1][16 * (g & 1)]);
 #pragma unroll
-            for (int c = 1; c < 32; ++c) mx[g] = fmaxf(mx[g], __uint_as_float(sr[g][c]));
+            for (int c = 1; c < 16; ++c) mx[g] = fmaxf(mx[g], __uint_as_float(sr[g >> 1][16 * (g & 1) + c]));
           }
-          float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+          // the row's maximum over both halves, through shared memory (buffers alternate: a
+          // warp two chunks ahead would have waited for this one in between)
+          float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          float* xc = xch + (chunk & 1) * 2 * MlaCfg::M;
+          xc[half * MlaCfg::M + h] = mc;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + C::B_MAX + quarter);
+          if (!mbar_wait(bars + C::B_MAX + quarter, chunk & 1, ab, 139)) { ok = false; break; }
+          mc = fmaxf(mc, xc[(half ^ 1) * MlaCfg::M + h]) * p.scale_log2;
           // the reference maximum moves only by more than 2^8 (P <= 256), so O is rarely rescaled
           float alpha = 1.f;
           if (mc > -INFINITY && (m_ref == -INFINITY || mc > m_ref + 8.f)) {
@@ -717,65 +724,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
           }
           const bool last = (j == sg.c1 - 1);
           if (!mbar_wait(bars + C::B_P_FREE + pb, pfree_ph, ab, 137)) { ok = false; break; }
-          uint8_t* st = smem + C::OFF_MSG + pb * C::MSG_STRIDE;
           // p = 2^(s scale log2e - m_ref) in bf16 into the swizzled P rows; the
           // row sum takes the unrounded fp32 values in eight partial sums
+          uint8_t* prow = smem + C::OFF_MSG + pb * C::P_BYTES + half * 16384 + h * 128;
           const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
           const float2 sl2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(neg_m, neg_m);
           float2 part[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) part[i] = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
+          for (int c8 = 0; c8 < 8; ++c8) {  // 8 keys = 16 bytes of the P row
+            uint32_t pk[4];
 #pragma unroll
-            for (int c4 = 0; c4 < 4; ++c4) {  // 8 keys = 16 bytes of the P row
-              uint32_t pk[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int c = c4 * 8 + 2 * i;
-                const float2 t = __ffma2_rn(make_float2(__uint_as_float(sr[g][c]), __uint_as_float(sr[g][c + 1])),
-                                            sl2, nm2);
-                const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
-                pk[i] = pack_bf16x2(e.x, e.y);
-                part[i] = __fadd2_rn(part[i], e);
-              }
-              const int c8 = g * 4 + c4;
-              const int kslab = c8 >> 3, cc = c8 & 7;
-              *reinterpret_cast<uint4*>(st + kslab * 16384 + h * 128 + ((cc ^ (h & 7)) << 4)) =
-                  make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            for (int i = 0; i < 4; ++i) {
+              const int c = (c8 & 3) * 8 + 2 * i;
+              const float2 t = __ffma2_rn(
+                  make_float2(__uint_as_float(sr[c8 >> 2][c]), __uint_as_float(sr[c8 >> 2][c + 1])), sl2, nm2);
+              const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+              pk[i] = pack_bf16x2(e.x, e.y);
+              part[i] = __fadd2_rn(part[i], e);
             }
+            *reinterpret_cast<uint4*>(prow + ((c8 ^ (h & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
           l_sum += ((part[0].x + part[0].y) + (part[1].x + part[1].y)) +
                    ((part[2].x + part[2].y) + (part[3].x + part[3].y));
-          reinterpret_cast<float*>(st + MlaCfg::MSG_ALPHA)[h] = alpha;
-          const uint32_t any_rs = __ballot_sync(0xffffffffu, alpha != 1.f);
-          if (lane == 0 && any_rs) atomicOr(rescale_s + (pb & 1), 1);
+          uint8_t* st = smem + C::OFF_STAT + pb * C::ST_STRIDE;
+          if (half == 0) {
+            reinterpret_cast<float*>(st + C::ST_ALPHA)[h] = alpha;
+            const uint32_t any_rs = __ballot_sync(0xffffffffu, alpha != 1.f);
+            if (lane == 0 && any_rs) atomicOr(rescale_s + (pb & 1), 1);
+          }
           if (last) {
-            reinterpret_cast<float*>(st + MlaCfg::MSG_L)[h] = l_sum;
-            reinterpret_cast<float*>(st + MlaCfg::MSG_M)[h] = m_ref;
+            reinterpret_cast<float*>(st + C::ST_L)[half * MlaCfg::M + h] = l_sum;
+            if (half == 0) reinterpret_cast<float*>(st + C::ST_M)[h] = m_ref;
           }
           fence_async_shared();
           __syncwarp();
           if (lane == 0) mbar_arrive(bars + C::B_STAGE);
           if (warp == C::W_SM0 && lane == 0) {
-            if (!mbar_wait(bars + C::B_STAGE, stage_ph, ab, 138)) ok = false;
+            if (!mbar_wait(bars + C::B_STAGE, chunk & 1, ab, 138)) ok = false;
             if (ok) {
-              uint32_t* ctrl = reinterpret_cast<uint32_t*>(st + MlaCfg::MSG_CTRL);
+              uint32_t* ctrl = reinterpret_cast<uint32_t*>(st + C::ST_CTRL);
               ctrl[0] = static_cast<uint32_t>(rescale_s[pb & 1]);
               rescale_s[pb & 1] = 0;
               fence_async_shared();
-              bulk_copy_to_peer(peer_msg + pb * C::MSG_STRIDE, smem_u32(st),
-                                last ? MlaCfg::MSG_BYTES_LAST : MlaCfg::MSG_BYTES_MID, peer_pfull + pb * 8);
+              bulk_copy_to_peer(peer_msg + pb * C::P_BYTES, msg + pb * C::P_BYTES, C::P_BYTES, peer_pfull + pb * 8);
+              bulk_copy_to_peer(peer_stat + pb * C::ST_STRIDE, smem_u32(st), last ? C::ST_BYTES_LAST : C::ST_BYTES_MID,
+                                peer_pfull + pb * 8);
             }
           }
-          stage_ph ^= 1;
           if (++pb == C::NPB) { pb = 0; pfree_ph ^= 1; }
           if (!ok) break;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars + C::B_MASK_FREE + mb);
       }
-    } else {
+    } else if (warp < C::W_SM0 + 4) {
       // ---- correction + epilogue ----
       int pb = 0;
       uint32_t pph = 0;
@@ -790,14 +792,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MlaQ4Cfg::NTHREADS, 
         float l_fin = 0.f, m_fin = -INFINITY;
         for (int j = sg.c0; j < sg.c1; ++j) {
           if (!mbar_wait(bars + C::B_P_FULL + pb, pph, ab, 145)) { ok = false; break; }
-          const uint8_t* mb = smem + C::OFF_MSG + pb * C::MSG_STRIDE;
-          const uint32_t any_rs = reinterpret_cast<const volatile uint32_t*>(mb + MlaCfg::MSG_CTRL)[0];
+          const uint8_t* mb = smem + C::OFF_STAT + pb * C::ST_STRIDE;
+          const uint32_t any_rs = reinterpret_cast<const volatile uint32_t*>(mb + C::ST_CTRL)[0];
           if (j == sg.c1 - 1) {
-            l_fin = reinterpret_cast<const float*>(mb + MlaCfg::MSG_L)[h];
-            m_fin = reinterpret_cast<const float*>(mb + MlaCfg::MSG_M)[h];
+            l_fin = reinterpret_cast<const float*>(mb + C::ST_L)[h] +
+                    reinterpret_cast<const float*>(mb + C::ST_L)[MlaCfg::M + h];
+            m_fin = reinterpret_cast<const float*>(mb + C::ST_M)[h];
           }
           if (any_rs && j > sg.c0) {
-            const float alpha = reinterpret_cast<const float*>(mb + MlaCfg::MSG_ALPHA)[h];
+            const float alpha = reinterpret_cast<const float*>(mb + C::ST_ALPHA)[h];
             if (!mbar_wait(bars + C::B_QUIESCE, qz_ph, ab, 146)) { ok = false; break; }
             qz_ph ^= 1;
             tc_fence_after();
