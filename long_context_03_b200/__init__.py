@@ -11,7 +11,6 @@ Build the library first with `python -m long_context_03_b200.build` (or
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -437,16 +436,35 @@ def dense_mla_attn_causal(q, kv, scale: float, *, q0: int = 0, out=None, lse=Non
 
 
 # ------------------------------------------------- the 4-bit latent cache and the norm in front of it
+#
+# These calls are made several times a layer with one token each, so their checks are kept to a few attribute
+# reads a tensor, pointers and the stream go to ctypes as integers, and all tensors have to be on one device, which
+# need not be the current one.
 
-def _on(device):
-    """Makes `device` the current one for a call (the library launches on the current device)."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _arg(t, name: str, dtype, shape, device) -> int:
+    """Address of a contiguous CUDA tensor of the given type, shape and device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr()
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _call(fn: str, device, *args):
+    """A library call on the current stream of `device`, made the current device for it."""
+    f = getattr(_lib or lib(), fn)
+    i = device.index
+    if torch.cuda.current_device() == i:
+        _check(f(*args, torch._C._cuda_getCurrentRawStream(i)))
+    else:
+        with torch.cuda.device(device):
+            _check(f(*args, torch._C._cuda_getCurrentRawStream(i)))
 
 
 def _rows(x, name):
@@ -476,33 +494,40 @@ def rms_norm_quantize_e4m3_rows(x, weight=None, *, residual=None, eps: float = 1
     x's type. summed is given back when there is a residual (or a tensor for it; residual itself serves in
     place), normed when want_normed (or a tensor for it); else None."""
     x_stride = _rows(x, "x")
-    n, d = x.shape
-    if residual is not None:
-        _req(residual, "residual", x.dtype, (n, d))
-    if weight is not None:
-        _req(weight, "weight", x.dtype, (d,))
+    dt, dev, shape = x.dtype, x.device, x.shape
+    n, d = shape
+    pr = None if residual is None else _arg(residual, "residual", dt, shape, dev)
+    pw = None if weight is None else _arg(weight, "weight", dt, (d,), dev)
     if codes is None:
-        codes = torch.empty((n, d), dtype=torch.uint8, device=x.device)
-    codes8 = _u8(codes)
-    _req(codes8, "codes", torch.uint8, (n, d))
-    shape = (n, -(-d // group)) if group > 0 else (n,)
+        codes = torch.empty(shape, dtype=torch.uint8, device=dev)
+    pc = _arg(_u8(codes), "codes", torch.uint8, shape, dev)
+    sshape = (n, -(-d // group)) if group > 0 else (n,)
     if scale is None:
-        scale = torch.empty(shape, dtype=torch.float32, device=x.device)
-    _req(scale, "scale", torch.float32, shape)
+        scale = torch.empty(sshape, dtype=torch.float32, device=dev)
+    ps = _arg(scale, "scale", torch.float32, sshape, dev)
     if summed is None and residual is not None:
-        summed = torch.empty((n, d), dtype=x.dtype, device=x.device)
-    if summed is not None:
-        _req(summed, "summed", x.dtype, (n, d))
+        summed = torch.empty(shape, dtype=dt, device=dev)
+    pm = None if summed is None else _arg(summed, "summed", dt, shape, dev)
     if normed is None and want_normed:
-        normed = torch.empty((n, d), dtype=x.dtype, device=x.device)
-    if normed is not None:
-        _req(normed, "normed", x.dtype, (n, d))
-    _same_device(x.device, residual=residual, weight=weight, codes=codes, scale=scale, summed=summed, normed=normed)
-    with _on(x.device):
-        _check(lib().dsa_rms_norm_quantize_e4m3_rows(_ptr(x), x_stride, _ptr(residual), _ptr(weight),
-                                                     _DTYPES[x.dtype], n, d, float(eps), group, _ptr(codes8),
-                                                     _ptr(scale), _ptr(summed), _ptr(normed), _stream(x.device)))
+        normed = torch.empty(shape, dtype=dt, device=dev)
+    pn = None if normed is None else _arg(normed, "normed", dt, shape, dev)
+    _call("dsa_rms_norm_quantize_e4m3_rows", dev, x.data_ptr(), x_stride, pr, pw, _DTYPES[dt], n, d, float(eps), group, pc,
+          ps, pm, pn)
     return codes, scale, summed, normed
+
+
+def _cache_arg(cache, name, device, lead=None):
+    """(address, rows) of a 4-bit cache [.., 416] (with the leading shape `lead` if given)."""
+    if not isinstance(cache, torch.Tensor) or not cache.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape = cache.shape
+    if len(shape) < 2 or shape[-1] != Q4_ROW_BYTES or (lead is not None and shape[:-1] != lead):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected rows of {Q4_ROW_BYTES} bytes")
+    p = _arg(cache, name, torch.uint8, shape, device)
+    rows = cache.numel() // Q4_ROW_BYTES
+    if rows >= 1 << 31:
+        raise ValueError(f"{name} has {rows} rows, at most 2^31 - 1 are addressed")
+    return p, rows
 
 
 def latent_q4_append(x, slots, pool):
@@ -510,83 +535,70 @@ def latent_q4_append(x, slots, pool):
     int32 of pool [.., 416] uint8 (any leading dimensions, counted as rows). A negative slot skips its row;
     the others must be distinct. Returns pool."""
     x_stride = _rows(x, "x")
-    n = x.shape[0]
-    if x.shape[1] != D_QK:
+    n, d = x.shape
+    if d != D_QK:
         raise ValueError(f"x has shape {tuple(x.shape)}, expected {(n, D_QK)}")
-    _req(slots, "slots", torch.int32, (n,))
-    rows = _req_q4(pool, "pool")
-    _same_device(x.device, slots=slots, pool=pool)
-    with _on(x.device):
-        _check(lib().dsa_latent_q4_append(_ptr(x), x_stride, _DTYPES[x.dtype], _ptr(slots), n, _ptr(pool), rows,
-                                          _stream(x.device)))
+    dev = x.device
+    ps = _arg(slots, "slots", torch.int32, (n,), dev)
+    pp, rows = _cache_arg(pool, "pool", dev)
+    _call("dsa_latent_q4_append", dev, x.data_ptr(), x_stride, _DTYPES[x.dtype], ps, n, pp, rows)
     return pool
 
 
 def latent_q4_gather(pool, rows, *, out=None):
     """Rows [n] int32 of a 4-bit cache pool [.., 416] as bf16 [n, 576] (exact; zeros for a negative row)."""
-    pool_rows = _req_q4(pool, "pool")
+    dev = pool.device
+    pp, pool_rows = _cache_arg(pool, "pool", dev)
     n = rows.shape[0]
-    _req(rows, "rows", torch.int32, (n,))
+    pr = _arg(rows, "rows", torch.int32, (n,), dev)
     if out is None:
-        out = torch.empty((n, D_QK), dtype=torch.bfloat16, device=pool.device)
-    _req(out, "out", torch.bfloat16, (n, D_QK))
-    _same_device(pool.device, rows=rows, out=out)
-    with _on(pool.device):
-        _check(lib().dsa_latent_q4_gather(_ptr(pool), pool_rows, _ptr(rows), n, _ptr(out), _stream(pool.device)))
+        out = torch.empty((n, D_QK), dtype=torch.bfloat16, device=dev)
+    _call("dsa_latent_q4_gather", dev, pp, pool_rows, pr, n, _arg(out, "out", torch.bfloat16, (n, D_QK), dev))
     return out
 
 
-def _req_q4(cache, name, lead=None) -> int:
-    """Checks a 4-bit cache [.., 416] (leading shape `lead` if given); its rows."""
-    _req(cache, name, torch.uint8)
-    if cache.dim() < 2 or cache.shape[-1] != Q4_ROW_BYTES or (lead is not None and tuple(cache.shape[:-1]) != lead):
-        raise ValueError(f"{name} has shape {tuple(cache.shape)}, expected rows of {Q4_ROW_BYTES} bytes")
-    rows = cache.numel() // Q4_ROW_BYTES
-    if rows >= 1 << 31:
-        raise ValueError(f"{name} has {rows} rows, at most 2^31 - 1 are addressed")
-    return rows
-
-
 def _q4_outputs(q, idx, out, lse, want_lse):
-    """Checks q and idx, makes out and lse where the caller gave none; (T, Hq, topk, out, lse)."""
+    """Checks q and idx, makes out and lse where the caller gave none: (device, T, Hq, topk, out, lse, addresses)."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
     T, Hq, _ = q.shape
     topk = idx.shape[1]
-    _req(q, "q", torch.bfloat16, (T, Hq, D_QK))
-    _req(idx, "idx", torch.int32, (T, topk))
+    dev = q.device
+    pq = _arg(q, "q", torch.bfloat16, (T, Hq, D_QK), dev)
+    pi = _arg(idx, "idx", torch.int32, (T, topk), dev)
     if out is None:
-        out = torch.empty((T, Hq, D_V), dtype=torch.bfloat16, device=q.device)
-    _req(out, "out", torch.bfloat16, (T, Hq, D_V))
+        out = torch.empty((T, Hq, D_V), dtype=torch.bfloat16, device=dev)
+    po = _arg(out, "out", torch.bfloat16, (T, Hq, D_V), dev)
     if lse is None and want_lse:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    if lse is not None:
-        _req(lse, "lse", torch.float32, (T, Hq))
-    return T, Hq, topk, out, lse
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    pl = None if lse is None else _arg(lse, "lse", torch.float32, (T, Hq), dev)
+    return dev, T, Hq, topk, out, lse, (pq, pi, po, pl)
+
+
+def _q4_split_ws(split, workspace, T, topk, device):
+    ws, ws_bytes = _split_ws(split, workspace, T, topk, device)
+    if ws is not None and ws.device != device:
+        raise ValueError(f"workspace is on {ws.device}, expected {device}")
+    return ws, (None if ws is None else ws.data_ptr()), ws_bytes
 
 
 def sparse_mla_attn_q4(q, kv_q4, idx, scale: float, *, out=None, lse=None, want_lse: bool = False):
     """sparse_mla_attn over a 4-bit cache kv_q4 [L, 416]: out [T, Hq, 512] bf16 (and lse [T, Hq] f32)."""
-    T, Hq, topk, out, lse = _q4_outputs(q, idx, out, lse, want_lse)
+    dev, T, Hq, topk, out, lse, (pq, pi, po, pl) = _q4_outputs(q, idx, out, lse, want_lse)
     L = kv_q4.shape[0]
-    _req_q4(kv_q4, "kv_q4", (L,))
-    _same_device(q.device, kv_q4=kv_q4, idx=idx, out=out, lse=lse)
-    with _on(q.device):
-        _check(lib().dsa_sparse_mla_attn_q4(_ptr(q), _ptr(kv_q4), _ptr(idx), T, L, Hq, topk, float(scale),
-                                            _ptr(out), _ptr(lse), _stream(q.device)))
+    pk, _ = _cache_arg(kv_q4, "kv_q4", dev, (L,))
+    _call("dsa_sparse_mla_attn_q4", dev, pq, pk, pi, T, L, Hq, topk, float(scale), po, pl)
     return out, lse
 
 
 def sparse_mla_attn_q4_decode(q, kv_q4, idx, scale: float, *, out=None, lse=None, want_lse: bool = False,
                               split: bool = True, workspace=None):
     """sparse_mla_attn_decode over a 4-bit cache kv_q4 [B, L_max, 416]."""
-    B, Hq, topk, out, lse = _q4_outputs(q, idx, out, lse, want_lse)
+    dev, B, Hq, topk, out, lse, (pq, pi, po, pl) = _q4_outputs(q, idx, out, lse, want_lse)
     L_max = kv_q4.shape[1]
-    _req_q4(kv_q4, "kv_q4", (B, L_max))
-    ws, ws_bytes = _split_ws(split, workspace, B, topk, q.device)
-    _same_device(q.device, kv_q4=kv_q4, idx=idx, out=out, lse=lse, workspace=ws)
-    with _on(q.device):
-        _check(lib().dsa_sparse_mla_attn_q4_decode(_ptr(q), _ptr(kv_q4), _ptr(idx), B, L_max, Hq, topk,
-                                                   float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
-                                                   _stream(q.device)))
+    pk, _ = _cache_arg(kv_q4, "kv_q4", dev, (B, L_max))
+    ws, pws, ws_bytes = _q4_split_ws(split, workspace, B, topk, dev)
+    _call("dsa_sparse_mla_attn_q4_decode", dev, pq, pk, pi, B, L_max, Hq, topk, float(scale), po, pl, pws, ws_bytes)
     return out, lse
 
 
@@ -594,39 +606,30 @@ def sparse_mla_attn_q4_paged(q, kv_q4_pool, block_table, idx, rows: int, scale: 
                              out=None, lse=None, want_lse: bool = False, split: bool = False, workspace=None):
     """sparse_mla_attn_paged over a pool [pool_rows, 416] of 4-bit rows; block_table [T, max_blocks] or
     [1, max_blocks] int32."""
-    T, Hq, topk, out, lse = _q4_outputs(q, idx, out, lse, want_lse)
+    dev, T, Hq, topk, out, lse, (pq, pi, po, pl) = _q4_outputs(q, idx, out, lse, want_lse)
     pool_rows = kv_q4_pool.shape[0]
     nbt, max_blocks = block_table.shape
-    _req_q4(kv_q4_pool, "kv_q4_pool", (pool_rows,))
-    _req(block_table, "block_table", torch.int32, (nbt, max_blocks))
+    pk, _ = _cache_arg(kv_q4_pool, "kv_q4_pool", dev, (pool_rows,))
+    pt = _arg(block_table, "block_table", torch.int32, (nbt, max_blocks), dev)
     if nbt not in (1, T):
         raise ValueError("block_table needs one row per token or a single shared row")
-    ws, ws_bytes = _split_ws(split, workspace, T, topk, q.device)
-    _same_device(q.device, kv_q4_pool=kv_q4_pool, block_table=block_table, idx=idx, out=out, lse=lse, workspace=ws)
-    with _on(q.device):
-        _check(lib().dsa_sparse_mla_attn_q4_paged(_ptr(q), _ptr(kv_q4_pool), _ptr(block_table), _ptr(idx), T, rows,
-                                                  pool_rows, 0 if nbt == 1 else max_blocks, max_blocks, page_size,
-                                                  Hq, topk, float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
-                                                  _stream(q.device)))
+    ws, pws, ws_bytes = _q4_split_ws(split, workspace, T, topk, dev)
+    _call("dsa_sparse_mla_attn_q4_paged", dev, pq, pk, pt, pi, T, rows, pool_rows, 0 if nbt == 1 else max_blocks,
+          max_blocks, page_size, Hq, topk, float(scale), po, pl, pws, ws_bytes)
     return out, lse
 
 
 def sparse_mla_attn_q4_varlen(q, kv_q4, idx, cu_q, cu_k, scale: float, *, out=None, lse=None,
                               want_lse: bool = False):
     """sparse_mla_attn_varlen over packed 4-bit rows kv_q4 [total_k, 416]."""
-    T, Hq, topk, out, lse = _q4_outputs(q, idx, out, lse, want_lse)
+    dev, T, Hq, topk, out, lse, (pq, pi, po, pl) = _q4_outputs(q, idx, out, lse, want_lse)
     total_k = kv_q4.shape[0]
-    cu_q = torch.as_tensor(cu_q, dtype=torch.int32, device=q.device).contiguous()
-    cu_k = torch.as_tensor(cu_k, dtype=torch.int32, device=q.device).contiguous()
+    cu_q = torch.as_tensor(cu_q, dtype=torch.int32, device=dev).contiguous()
+    cu_k = torch.as_tensor(cu_k, dtype=torch.int32, device=dev).contiguous()
     nseq = cu_q.numel() - 1
-    _req_q4(kv_q4, "kv_q4", (total_k,))
-    _req(cu_q, "cu_q", torch.int32, (nseq + 1,))
-    _req(cu_k, "cu_k", torch.int32, (nseq + 1,))
-    _same_device(q.device, kv_q4=kv_q4, idx=idx, out=out, lse=lse)
-    with _on(q.device):
-        _check(lib().dsa_sparse_mla_attn_q4_varlen(_ptr(q), _ptr(kv_q4), _ptr(idx), _ptr(cu_q), _ptr(cu_k), nseq, T,
-                                                   total_k, Hq, topk, float(scale), _ptr(out), _ptr(lse),
-                                                   _stream(q.device)))
+    pk, _ = _cache_arg(kv_q4, "kv_q4", dev, (total_k,))
+    _call("dsa_sparse_mla_attn_q4_varlen", dev, pq, pk, pi, _arg(cu_q, "cu_q", torch.int32, (nseq + 1,), dev),
+          _arg(cu_k, "cu_k", torch.int32, (nseq + 1,), dev), nseq, T, total_k, Hq, topk, float(scale), po, pl)
     return out, lse
 
 

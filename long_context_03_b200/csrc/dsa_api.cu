@@ -587,19 +587,24 @@ dsa_status check_mla_q4_args(const uint16_t* q, const uint8_t* cache, const int3
 }
 
 // ---- norm ----
-template <typename T, bool kGroup>
+template <typename T, bool kVec, bool kGroup>
 void launch_norm(const NormParams& p, cudaStream_t st) {
   // One warp holds a row of up to 1024 values, one block a longer one.
   auto go = [&](auto kern, int rows_per_block) {
     kern<<<(p.n + rows_per_block - 1) / rows_per_block, kNormThreads, 0, st>>>(p);
   };
-  if (p.d <= 256) go(rms_norm_quantize_kernel<T, 32, 1, kGroup>, 8);
-  else if (p.d <= 512) go(rms_norm_quantize_kernel<T, 32, 2, kGroup>, 8);
-  else if (p.d <= 1024) go(rms_norm_quantize_kernel<T, 32, 4, kGroup>, 8);
-  else if (p.d <= 2048) go(rms_norm_quantize_kernel<T, 256, 1, kGroup>, 1);
-  else if (p.d <= 4096) go(rms_norm_quantize_kernel<T, 256, 2, kGroup>, 1);
-  else if (p.d <= 8192) go(rms_norm_quantize_kernel<T, 256, 4, kGroup>, 1);
-  else go(rms_norm_quantize_kernel<T, 256, 8, kGroup>, 1);
+  if (p.d <= 256) go(rms_norm_quantize_kernel<T, 32, 1, kVec, kGroup>, 8);
+  else if (p.d <= 512) go(rms_norm_quantize_kernel<T, 32, 2, kVec, kGroup>, 8);
+  else if (p.d <= 1024) go(rms_norm_quantize_kernel<T, 32, 4, kVec, kGroup>, 8);
+  else if (p.d <= 2048) go(rms_norm_quantize_kernel<T, 256, 1, kVec, kGroup>, 1);
+  else if (p.d <= 4096) go(rms_norm_quantize_kernel<T, 256, 2, kVec, kGroup>, 1);
+  else if (p.d <= 8192) go(rms_norm_quantize_kernel<T, 256, 4, kVec, kGroup>, 1);
+  else go(rms_norm_quantize_kernel<T, 256, 8, kVec, kGroup>, 1);
+}
+template <typename T>
+void dispatch_norm(const NormParams& p, bool vec, bool group, cudaStream_t st) {
+  if (vec) group ? launch_norm<T, true, true>(p, st) : launch_norm<T, true, false>(p, st);
+  else group ? launch_norm<T, false, true>(p, st) : launch_norm<T, false, false>(p, st);
 }
 
 int dtype_size(int dtype) { return dtype == DSA_F32 ? 4 : (dtype == DSA_BF16 || dtype == DSA_F16) ? 2 : 0; }
@@ -1029,12 +1034,12 @@ dsa_status dsa_rms_norm_quantize_e4m3_rows(const void* x, long long x_stride, co
   p.n = n;
   p.d = d;
   p.eps = eps;
-  p.vec = d % 8 == 0 && (x_stride * es) % 16 == 0 && aligned16(x) && aligned16(residual) && aligned16(weight) &&
+  const bool vec = d % 8 == 0 && (x_stride * es) % 16 == 0 && aligned16(x) && aligned16(residual) && aligned16(weight) &&
           aligned16(summed) && aligned16(normed) && (reinterpret_cast<uintptr_t>(codes) & 7u) == 0;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == DSA_F32) group ? launch_norm<float, true>(p, st) : launch_norm<float, false>(p, st);
-  else if (dtype == DSA_BF16) group ? launch_norm<__nv_bfloat16, true>(p, st) : launch_norm<__nv_bfloat16, false>(p, st);
-  else group ? launch_norm<__half, true>(p, st) : launch_norm<__half, false>(p, st);
+  if (dtype == DSA_F32) dispatch_norm<float>(p, vec, group != 0, st);
+  else if (dtype == DSA_BF16) dispatch_norm<__nv_bfloat16>(p, vec, group != 0, st);
+  else dispatch_norm<__half>(p, vec, group != 0, st);
   return check_launch("rms_norm_quantize_kernel");
 }
 

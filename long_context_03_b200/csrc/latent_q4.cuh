@@ -94,6 +94,19 @@ __device__ __forceinline__ int q4_code(float x, float s, float inv) {
   return x == x ? static_cast<int>(r) : 0;
 }
 
+// The same for a finite x of at most 11 significant bits (bf16, f16) with
+// |x| <= 7 s, as the low four bits of the result, which are the code: x / s
+// correctly rounded (quotient estimate, exact remainder, one correction:
+// Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990) is exact at a tie and, with so few bits against the four
+// of s, nowhere else next to one; adding 1.5 * 2^23 + 8 rounds it to an
+// integer, ties to even.
+__device__ __forceinline__ uint32_t q4_code_short(float x, float s, float inv) {
+  const float q = x * inv;
+  const float r = __fmaf_rn(__fmaf_rn(-q, s, x), inv, q);
+  return __float_as_uint(r + 12582920.f);
+}
+
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
@@ -160,17 +173,31 @@ __global__ void __launch_bounds__(kQ4Threads)
   r0 = to_f32(xr[kQ4Latent + 2 * lane]);
   r1 = to_f32(xr[kQ4Latent + 2 * lane + 1]);
   float amax = 0.f;
+  uint32_t top = 0;  // the largest magnitude's bits, NaN and infinity included
 #pragma unroll
-  for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(v[k]));  // fmaxf passes a NaN over
+  for (int k = 0; k < 16; ++k) {
+    amax = fmaxf(amax, fabsf(v[k]));  // fmaxf passes a NaN over
+    top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
+  }
   const int b = q4_scale_byte(amax);
   const float s = q4_scale_f32(b), inv = __frcp_rn(s);
   uint32_t w[2];
+  // value j of a word is nibble j / 2 or 4 + j / 2; the highest nibble first
+  constexpr int kOrder[8] = {7, 5, 3, 1, 6, 4, 2, 0};
+  if (sizeof(T) == 2 && top < 0x7f800000u && amax <= 7.f * s) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    w[h] = 0;
+    for (int h = 0; h < 2; ++h) {
+      w[h] = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      w[h] |= static_cast<uint32_t>(q4_code(v[8 * h + j], s, inv) + 8) << (4 * ((j >> 1) + 4 * (j & 1)));
+      for (int j = 0; j < 8; ++j) w[h] = (w[h] << 4) | (q4_code_short(v[8 * h + kOrder[j]], s, inv) & 15u);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      w[h] = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[h] = (w[h] << 4) | static_cast<uint32_t>(q4_code(v[8 * h + kOrder[j]], s, inv) + 8);
+    }
   }
   uint8_t* row = pool + static_cast<size_t>(slot) * kQ4RowBytes;
   reinterpret_cast<uint2*>(row)[lane] = make_uint2(w[0], w[1]);

@@ -52,9 +52,65 @@ __device__ __forceinline__ void from_f32(float* p, float v) { *p = v; }
 __device__ __forceinline__ void from_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void from_f32(__half* p, float v) { *p = __float2half_rn(v); }
 
-__device__ __forceinline__ uint8_t e4m3_code(float y, float sc) {
-  const float q = fminf(fmaxf(__fdiv_rn(y, sc), -448.f), 448.f);
-  return static_cast<uint8_t>(__nv_cvt_float_to_fp8(y == y ? q : y, __NV_SATFINITE, __NV_E4M3));
+// y / sc correctly rounded, for a divisor that serves many dividends: with
+// inv = 1 / sc correctly rounded, q = y inv is within an ulp of the quotient,
+// r = y - q sc is exact in a fused multiply-add, and q + r inv rounds to the
+// quotient (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990). With a divisor so small or large that r could
+// underflow (`far`) the plain division is taken.
+struct RowScale {
+  float sc, inv;
+  bool far;
+};
+__device__ __forceinline__ RowScale row_scale(float amax) {
+  RowScale s;
+  s.sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+  s.inv = __frcp_rn(s.sc);
+  s.far = !(s.sc > 1e-25f && s.sc < 1e30f);
+  return s;
+}
+template <int N>
+__device__ __forceinline__ void scale_all(float (&y)[N], const RowScale& s) {
+  if (s.far) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) y[k] = __fdiv_rn(y[k], s.sc);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float q = y[k] * s.inv;
+      y[k] = __fmaf_rn(__fmaf_rn(-q, s.sc, y[k]), s.inv, q);
+    }
+  }
+}
+// E4M3 codes of two numbers: nearest, ties to even, saturating; a NaN stays one.
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Rows stream through once: their lines are marked to leave the caches first,
+// so that the weights stay in L1.
+__device__ __forceinline__ void load8_stream(const float* p, float (&v)[8]) {
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p + 4));
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8_stream(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8_stream(const __half* p, float (&v)[8]) {
+  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
 }
 
 struct NormParams {
@@ -68,13 +124,13 @@ struct NormParams {
   long long x_stride;
   int n, d;
   float eps;
-  bool vec;              // every row is 16-byte aligned and d % 8 == 0
 };
 
-// kGroup: a scale for each 128 values instead of one for the row. Without
-// alignment (vec false) the threads take single elements, neighbours next to
-// each other, and only the map from registers to elements differs.
-template <typename T, int kTpr, int kNv, bool kGroup>
+// kVec: every row is 16-byte aligned and d a multiple of 8. Without it the
+// threads take single elements, neighbours next to each other, and only the
+// map from registers to elements differs. kGroup: a scale for each 128 values
+// instead of one for the row.
+template <typename T, int kTpr, int kNv, bool kVec, bool kGroup>
 __global__ void __launch_bounds__(kNormThreads) rms_norm_quantize_kernel(const NormParams p) {
   constexpr int kRows = kNormThreads / kTpr;  // rows of a block
   constexpr int kWarps = kTpr / 32;           // warps of a row
@@ -92,7 +148,7 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_quantize_kernel(const N
   const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
   const T* res = p.residual ? static_cast<const T*>(p.residual) + row * d : nullptr;
   const T* wt = static_cast<const T*>(p.weight);
-  auto at = [&](int i, int k) { return p.vec ? (t + kTpr * i) * 8 + k : (i * 8 + k) * kTpr + t; };
+  auto at = [&](int i, int k) { return kVec ? (t + kTpr * i) * 8 + k : (i * 8 + k) * kTpr + t; };
   auto row_sync = [&]() {
     if constexpr (kWarps > 1) __syncthreads();
     else __syncwarp();
@@ -101,13 +157,13 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_quantize_kernel(const N
   float h[kNv][8];
 #pragma unroll
   for (int i = 0; i < kNv; ++i) {
-    if (p.vec) {
+    if constexpr (kVec) {
       const int e = at(i, 0);
       if (e < d) {
-        load8(x + e, h[i]);
+        load8_stream(x + e, h[i]);
         if (res) {
           float r[8];
-          load8(res + e, r);
+          load8_stream(res + e, r);
 #pragma unroll
           for (int k = 0; k < 8; ++k) h[i][k] += r[k];
         }
@@ -151,7 +207,7 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_quantize_kernel(const N
     T* o = static_cast<T*>(p.summed) + row * d;
 #pragma unroll
     for (int i = 0; i < kNv; ++i) {
-      if (p.vec) {
+      if constexpr (kVec) {
         if (at(i, 0) < d) store8(o + at(i, 0), h[i]);
       } else {
 #pragma unroll
@@ -160,13 +216,12 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_quantize_kernel(const N
       }
     }
   }
-  // y in place of h, and the largest magnitudes (fmaxf passes NaN over, as
-  // the plain quantiser does: such a value's code is NaN, its scale the others')
+  // y in place of h, and the largest magnitudes (fmaxf passes NaN over)
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < kNv; ++i) {
     float wv[8];
-    if (p.vec) {
+    if constexpr (kVec) {
       if (wt && at(i, 0) < d) {
         load8(wt + at(i, 0), wv);
       } else {
@@ -183,7 +238,7 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_quantize_kernel(const N
       h[i][k] = h[i][k] * rstd * wv[k];
       m = fmaxf(m, fabsf(h[i][k]));
       if constexpr (kGroup) {
-        if (!p.vec) {
+        if constexpr (!kVec) {
           // 32 neighbouring elements lie in one group (magnitudes compare as their bits)
           const uint32_t mk = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(0.f, fabsf(h[i][k]))));
           if (lane == 0 && at(i, k) < d) atomicMax(&gmax[sub][at(i, k) / kNormGroup], mk);
@@ -191,7 +246,7 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_quantize_kernel(const N
       }
     }
     if constexpr (kGroup) {
-      if (p.vec) {
+      if constexpr (kVec) {
         // 16 neighbouring threads hold a group
 #pragma unroll
         for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -201,13 +256,13 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_quantize_kernel(const N
       amax = fmaxf(amax, m);
     }
   }
-  float sc = 1.f;
+  RowScale sc = row_scale(0.f);
   if constexpr (kGroup) {
     row_sync();
     const int groups = (d + kNormGroup - 1) / kNormGroup;
     for (int g = t; g < groups; g += kTpr) {
       const float m = __uint_as_float(gmax[sub][g]);
-      p.scale[row * groups + g] = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+      p.scale[row * groups + g] = row_scale(m).sc;
     }
   } else {
 #pragma unroll
@@ -219,24 +274,25 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_quantize_kernel(const N
 #pragma unroll
       for (int j = 1; j < kWarps; ++j) amax = fmaxf(amax, redm[sub][j]);
     }
-    sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
-    if (t == 0) p.scale[row] = sc;
+    sc = row_scale(amax);
+    if (t == 0) p.scale[row] = sc.sc;
   }
   uint8_t* cr = p.codes + row * d;
   T* no = p.normed ? static_cast<T*>(p.normed) + row * d : nullptr;
 #pragma unroll
   for (int i = 0; i < kNv; ++i) {
-    if (p.vec) {
+    if constexpr (kVec) {
       const int e = at(i, 0);
       if (e >= d) continue;
       if constexpr (kGroup) {
-        const float m = __uint_as_float(gmax[sub][e / kNormGroup]);
-        sc = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+        sc = row_scale(__uint_as_float(gmax[sub][e / kNormGroup]));
       }
       if (no) store8(no + e, h[i]);
-      uint32_t c[2] = {0, 0};
+      scale_all(h[i], sc);
+      uint32_t c[2];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) c[k >> 2] |= static_cast<uint32_t>(e4m3_code(h[i][k], sc)) << (8 * (k & 3));
+      for (int k = 0; k < 2; ++k)
+        c[k] = e4m3_pair(h[i][4 * k], h[i][4 * k + 1]) | e4m3_pair(h[i][4 * k + 2], h[i][4 * k + 3]) << 16;
       *reinterpret_cast<uint2*>(cr + e) = make_uint2(c[0], c[1]);
     } else {
 #pragma unroll
@@ -244,11 +300,12 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_quantize_kernel(const N
         const int e = at(i, k);
         if (e >= d) continue;
         if constexpr (kGroup) {
-          const float m = __uint_as_float(gmax[sub][e / kNormGroup]);
-          sc = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+          sc = row_scale(__uint_as_float(gmax[sub][e / kNormGroup]));
         }
         if (no) from_f32(no + e, h[i][k]);
-        cr[e] = e4m3_code(h[i][k], sc);
+        float y[1] = {h[i][k]};
+        scale_all(y, sc);
+        cr[e] = static_cast<uint8_t>(e4m3_pair(y[0], 0.f));
       }
     }
   }
