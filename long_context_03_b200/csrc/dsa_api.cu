@@ -520,6 +520,23 @@ int mla_q4_max_clusters() {
   return n;
 }
 
+// Whether both instances launch with the registers that their warp groups
+// trade (a group that asks for more than the block has would wait forever).
+// A property of the build, looked up once.
+bool mla_q4_registers_ok() {
+  static std::atomic<int> cache{0};
+  int v = cache.load(std::memory_order_relaxed);
+  if (v == 0) {
+    cudaFuncAttributes a = {}, b = {};
+    const bool ok = cudaFuncGetAttributes(&a, sparse_mla_q4_kernel<false>) == cudaSuccess &&
+                    cudaFuncGetAttributes(&b, sparse_mla_q4_kernel<true>) == cudaSuccess &&
+                    a.numRegs >= MlaQ4Cfg::REG_LAUNCH && b.numRegs >= MlaQ4Cfg::REG_LAUNCH;
+    v = ok ? 1 : 2;
+    cache.store(v, std::memory_order_relaxed);
+  }
+  return v == 1;
+}
+
 dsa_status launch_mla_q4(const uint16_t* q, const uint8_t* cache, const int32_t* idx, int T, int rows,
                          long long token_rows, int Hq, int topk, float scale, uint16_t* out, float* lse,
                          cudaStream_t st, MlaPaging pg = MlaPaging(), MlaPacked pk = MlaPacked(),
@@ -552,6 +569,9 @@ dsa_status launch_mla_q4(const uint16_t* q, const uint8_t* cache, const int32_t*
   auto kern = pg.block_table ? sparse_mla_q4_kernel<true> : sparse_mla_q4_kernel<false>;
   s = set_smem(kern, MlaQ4Cfg::SMEM_BYTES);
   if (s != DSA_OK) return s;
+  if (!mla_q4_registers_ok())
+    return fail(DSA_ERR_CUDA, "the 4-bit attention kernel was built with fewer than %d registers a thread, which its "
+                "warps' register trade needs", MlaQ4Cfg::REG_LAUNCH);
   const int max_clusters = mla_q4_max_clusters();
   const int nchunk = (topk + MlaCfg::NK - 1) / MlaCfg::NK;
   const long long units = static_cast<long long>(T) * nchunk;
@@ -591,7 +611,7 @@ template <typename T, bool kVec, bool kGroup>
 void launch_norm(const NormParams& p, cudaStream_t st) {
   // One warp holds a row of up to 1024 values, one block a longer one.
   auto go = [&](auto kern, int rows_per_block) {
-    kern<<<(p.n + rows_per_block - 1) / rows_per_block, kNormThreads, 0, st>>>(p);
+    kern<<<p.n / rows_per_block + (p.n % rows_per_block ? 1 : 0), kNormThreads, 0, st>>>(p);
   };
   if (p.d <= 256) go(rms_norm_quantize_kernel<T, 32, 1, kVec, kGroup>, 8);
   else if (p.d <= 512) go(rms_norm_quantize_kernel<T, 32, 2, kVec, kGroup>, 8);

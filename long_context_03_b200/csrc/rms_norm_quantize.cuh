@@ -12,6 +12,13 @@
 // A row is read once: its values stay in registers between the two
 // reductions (sum of squares, largest magnitude) and the output. kTpr threads
 // hold a row, kNv groups of 8 values each.
+//
+// Bound: memory for many rows, with the two reductions of each row between its
+// loads and its stores; latency for few. Measured on bf16 rows of 7168 with a
+// residual: 16384 rows 180 us (4.6 TB/s, 70% of a copy's rate); 255 us with a
+// division a value and the aligned and unaligned paths in one kernel. Rows of
+// up to 1024 values take a warp (no block barrier: 16384 rows of 512 in 10.8
+// us), longer ones a block.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -297,3 +297,32 @@ def test_a_serving_step_end_to_end(dsa):
     graph.replay()
     torch.cuda.synchronize()
     check(*outs)
+
+
+def test_empty_batches(dsa):
+    pool = _cache(8, 91).cuda()
+    q = torch.empty((0, 16, 576), dtype=torch.bfloat16, device="cuda")
+    idx = torch.empty((0, 4), dtype=torch.int32, device="cuda")
+    out, lse = dsa.sparse_mla_attn_q4(q, pool, idx, SCALE, want_lse=True)
+    assert out.shape == (0, 16, 512) and lse.shape == (0, 16)
+    dsa.check_device_error()
+
+
+def test_two_streams_at_once(dsa):
+    pool = _cache(3000, 95).cuda()
+    work = []
+    for s in range(2):
+        q = _queries(80, 128, 96 + s).cuda()
+        idx = _selection([3000 - 7 * t for t in range(80)], 700, 97 + s).cuda()
+        work.append((q, idx, dsa.sparse_mla_attn_q4(q, pool, idx, SCALE, want_lse=True), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(4):
+        for q, idx, _, stream in work:
+            with torch.cuda.stream(stream):
+                outs.append(dsa.sparse_mla_attn_q4(q, pool, idx, SCALE, want_lse=True))
+    torch.cuda.synchronize()
+    dsa.check_device_error()
+    for i, (out, lse) in enumerate(outs):
+        ref, ref_lse = work[i % 2][2]
+        assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
