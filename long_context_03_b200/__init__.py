@@ -498,19 +498,32 @@ def rms_norm_quantize_e4m3_rows(x, weight=None, *, residual=None, eps: float = 1
     n, d = shape
     pr = None if residual is None else _arg(residual, "residual", dt, shape, dev)
     pw = None if weight is None else _arg(weight, "weight", dt, (d,), dev)
+    # (new outputs need no checks, and empty_like is the quicker way to make them)
     if codes is None:
-        codes = torch.empty(shape, dtype=torch.uint8, device=dev)
-    pc = _arg(_u8(codes), "codes", torch.uint8, shape, dev)
+        codes = torch.empty_like(x, dtype=torch.uint8, memory_format=torch.contiguous_format)
+        pc = codes.data_ptr()
+    else:
+        pc = _arg(_u8(codes), "codes", torch.uint8, shape, dev)
     sshape = (n, -(-d // group)) if group > 0 else (n,)
     if scale is None:
         scale = torch.empty(sshape, dtype=torch.float32, device=dev)
-    ps = _arg(scale, "scale", torch.float32, sshape, dev)
-    if summed is None and residual is not None:
-        summed = torch.empty(shape, dtype=dt, device=dev)
-    pm = None if summed is None else _arg(summed, "summed", dt, shape, dev)
-    if normed is None and want_normed:
-        normed = torch.empty(shape, dtype=dt, device=dev)
-    pn = None if normed is None else _arg(normed, "normed", dt, shape, dev)
+        ps = scale.data_ptr()
+    else:
+        ps = _arg(scale, "scale", torch.float32, sshape, dev)
+    if summed is not None:
+        pm = _arg(summed, "summed", dt, shape, dev)
+    elif residual is not None:
+        summed = torch.empty_like(residual)
+        pm = summed.data_ptr()
+    else:
+        pm = None
+    if normed is not None:
+        pn = _arg(normed, "normed", dt, shape, dev)
+    elif want_normed:
+        normed = torch.empty_like(x, memory_format=torch.contiguous_format)
+        pn = normed.data_ptr()
+    else:
+        pn = None
     _call("dsa_rms_norm_quantize_e4m3_rows", dev, x.data_ptr(), x_stride, pr, pw, _DTYPES[dt], n, d, float(eps), group, pc,
           ps, pm, pn)
     return codes, scale, summed, normed
@@ -553,7 +566,10 @@ def latent_q4_gather(pool, rows, *, out=None):
     pr = _arg(rows, "rows", torch.int32, (n,), dev)
     if out is None:
         out = torch.empty((n, D_QK), dtype=torch.bfloat16, device=dev)
-    _call("dsa_latent_q4_gather", dev, pp, pool_rows, pr, n, _arg(out, "out", torch.bfloat16, (n, D_QK), dev))
+        po = out.data_ptr()
+    else:
+        po = _arg(out, "out", torch.bfloat16, (n, D_QK), dev)
+    _call("dsa_latent_q4_gather", dev, pp, pool_rows, pr, n, po)
     return out
 
 
@@ -568,10 +584,16 @@ def _q4_outputs(q, idx, out, lse, want_lse):
     pi = _arg(idx, "idx", torch.int32, (T, topk), dev)
     if out is None:
         out = torch.empty((T, Hq, D_V), dtype=torch.bfloat16, device=dev)
-    po = _arg(out, "out", torch.bfloat16, (T, Hq, D_V), dev)
-    if lse is None and want_lse:
+        po = out.data_ptr()
+    else:
+        po = _arg(out, "out", torch.bfloat16, (T, Hq, D_V), dev)
+    if lse is not None:
+        pl = _arg(lse, "lse", torch.float32, (T, Hq), dev)
+    elif want_lse:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-    pl = None if lse is None else _arg(lse, "lse", torch.float32, (T, Hq), dev)
+        pl = lse.data_ptr()
+    else:
+        pl = None
     return dev, T, Hq, topk, out, lse, (pq, pi, po, pl)
 
 
